@@ -194,6 +194,79 @@ la_status la_decode_step(const void *q, const void *k, const void *v, float *sta
 la_status la_state_out(const float *state_ws, float *state_dst, int S, int H, int D,
                        const int32_t *seq_to_slot, int num_slots, void *stream);
 
+/*
+ * Gated lightning attention: the state decays by e^{g_t} before token t is added,
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t,
+ *
+ * with one log-decay g per token and head (natural logarithm; usually <= 0).  g = 0 (or
+ * g == NULL) is the ungated recurrence of la_prefill and la_decode_step.  g = -inf forgets
+ * the state (values below -1000 count as -1000: e^-1000 is 0).
+ *
+ *   g         [T][H], the dtype of q; NULL: no decay.  Element-aligned.
+ *   flags     LA_BF16 or LA_FP32 alone.
+ *   workspace device memory of at least the bytes that la_gated_workspace names for the
+ *             same shape, owned by the caller and free again when the work enqueued by the
+ *             call has run.  A call overwrites it without reading what is in it: two calls
+ *             that may run at the same time need two workspaces.
+ *   B, H, N, D, cu_seqlens, num_seqs as in la_prefill.
+ *
+ * Non-finite values in a sequence may reach every row of that sequence in either direction
+ * of time (block products multiply masked entries by 0), but no other sequence.
+ */
+
+/* Bytes of workspace of la_gated_prefill (backward == 0) or la_gated_prefill_backward
+ * (backward != 0) for this shape and these flags. */
+la_status la_gated_workspace(int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs,
+                             unsigned flags, int backward, unsigned long long *bytes);
+
+/*
+ * la_gated_prefill -- o and, with state_out, the final state of every sequence.
+ *
+ *   state_in  [S][H][D][D] fp32: the sequences' initial states, or NULL for zero.
+ *   state_out [S][H][D][D] fp32 or NULL: the final states; may be state_in itself (update
+ *             in place), but not overlap it otherwise.  A sequence of no tokens keeps its
+ *             initial state.
+ */
+la_status la_gated_prefill(const void *q, const void *k, const void *v, const void *g, void *o,
+                           int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs,
+                           unsigned flags, const float *state_in, float *state_out,
+                           void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/*
+ * la_gated_prefill_backward -- gradients of la_gated_prefill's inputs.
+ *
+ *   dout       [T][H][D]: gradient of o.
+ *   d_state    [S][H][D][D] fp32 or NULL: gradient of the final states.
+ *   dq, dk, dv [T][H][D], dg [T][H] (or NULL), in the dtype of q; they overlap no input.
+ *   d_state_in [S][H][D][D] fp32 or NULL: gradient of the initial states; may be d_state
+ *              itself.
+ * The states are recomputed from k, v, g and state_in.  With g == NULL these are the
+ * gradients of la_prefill without LA_OUT_RMSNORM.  Every sum has a fixed order: equal
+ * inputs give equal bits.
+ */
+la_status la_gated_prefill_backward(const void *q, const void *k, const void *v, const void *g,
+                                    const void *dout, void *dq, void *dk, void *dv, void *dg,
+                                    int B, int H, int N, int D, const int32_t *cu_seqlens,
+                                    int num_seqs, unsigned flags, const float *state_in,
+                                    const float *d_state, float *d_state_in, void *workspace,
+                                    unsigned long long workspace_bytes, void *stream);
+
+/*
+ * la_gated_decode_step -- one token per row: state <- e^g state + k v^T, o = state^T q.
+ *
+ *   q, k, v, o [B][H][D]; g [B][H] or NULL.
+ *   state      [num_slots][H][D][D] fp32, updated in place.
+ *   slots      DEVICE array of B int32: the state of row b is slots[b].  -1 marks a padding
+ *              row, of which nothing is read or written.  A slot outside the pool, and one
+ *              that an earlier row of the call has, are skipped in the same way and reported
+ *              as LA_ERR_DEVICE_RANGE by la_get_device_status.  NULL: row b has slot b (then
+ *              B <= num_slots).
+ */
+la_status la_gated_decode_step(const void *q, const void *k, const void *v, const void *g,
+                               float *state, void *o, int B, int H, int D, const int32_t *slots,
+                               int num_slots, unsigned flags, void *stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *la_status_string(la_status status);
 

@@ -8,9 +8,10 @@ this package does not load the library; the first call does, and fails loudly
 if it is missing.
 """
 from .api import (LA_BF16, LA_FP32, LA_OUT_RMSNORM, LA_WRITE_STATE, LightningError,
-                  LightningLibraryError, decode_step, device_status, lib, prefill, state_out,
-                  status_string, version)
+                  LightningLibraryError, decode_step, device_status, gated_decode_step,
+                  gated_prefill, gated_prefill_backward, lib, prefill, state_out, status_string,
+                  version)
 
-__all__ = ["prefill", "decode_step", "state_out", "device_status", "lib", "status_string",
-           "version", "LightningError", "LightningLibraryError", "LA_BF16", "LA_FP32",
+__all__ = ["prefill", "decode_step", "state_out", "device_status", "gated_prefill",
+           "gated_prefill_backward", "gated_decode_step", "lib", "status_string", "version", "LightningError", "LightningLibraryError", "LA_BF16", "LA_FP32",
            "LA_OUT_RMSNORM", "LA_WRITE_STATE"]

@@ -8,6 +8,7 @@ a missing or unloadable library raises ``LightningLibraryError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -62,6 +63,16 @@ def lib() -> ctypes.CDLL:
     L.la_chunk_state.restype = i32
     L.la_state_prefix.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp]
     L.la_state_prefix.restype = i32
+    u64 = ctypes.c_ulonglong
+    L.la_gated_workspace.argtypes = [i32, i32, i32, i32, ip, i32, u32, i32, ctypes.POINTER(u64)]
+    L.la_gated_workspace.restype = i32
+    L.la_gated_prefill.argtypes = [vp] * 5 + [i32] * 4 + [ip, i32, u32, vp, vp, vp, u64, vp]
+    L.la_gated_prefill.restype = i32
+    L.la_gated_prefill_backward.argtypes = ([vp] * 9 + [i32] * 4 +
+                                            [ip, i32, u32, vp, vp, vp, vp, u64, vp])
+    L.la_gated_prefill_backward.restype = i32
+    L.la_gated_decode_step.argtypes = [vp] * 6 + [i32] * 3 + [vp, i32, u32, vp]
+    L.la_gated_decode_step.restype = i32
     L.la_selftest_wait.argtypes = [ctypes.c_ulonglong, vp]
     L.la_selftest_wait.restype = i32
     L.la_status_string.argtypes = [i32]
@@ -337,6 +348,176 @@ def state_prefix(gathered, rank: int, *, out=None, stream=None):
         rc = lib().la_state_prefix(_ptr(gathered), R, int(rank), S, H, D, _ptr(out),
                                    _stream_ptr(stream))
     _check("la_state_prefix", rc)
+    return out
+
+
+def _gated_shape(q, k, v, g, cu_seqlens):
+    """Checks the sequence operators share; (B, H, N, D, S, boundaries or None)."""
+    _need(q, "q")
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, q.dtype, q.device)
+        if t.shape != q.shape:
+            raise ValueError("q, k, v must have one shape")
+    if q.dim() == 4:
+        B, N, H, D = q.shape
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens needs packed [T, H, D] inputs")
+        S = B
+    elif q.dim() == 3:
+        N, H, D = q.shape
+        B, S = 1, 1 if cu_seqlens is None else len(cu_seqlens) - 1
+    else:
+        raise ValueError("q must be [B, N, H, D] or [T, H, D]")
+    if g is not None:
+        _need(g, "g", q.dtype, q.device)
+        _need_shape(g, "g", q.shape[:-1])
+    cu = None if cu_seqlens is None else np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    return B, H, N, D, S, cu
+
+
+def _need_state(t, name, shape, dev):
+    if t is not None:
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, shape)
+
+
+def _gated_workspace(args, cu_ptr, num_seqs, flags, backward, dev, stream):
+    """The call's workspace, from the caching allocator's pool of the stream it runs on: the
+    block is not handed to another stream while the call's kernels may still use it."""
+    n = ctypes.c_ulonglong()
+    _check("la_gated_workspace",
+           lib().la_gated_workspace(*args, cu_ptr, num_seqs, flags, backward, ctypes.byref(n)))
+    if n.value == 0:
+        return None, 0
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+
+
+def _used_on(stream, *tensors):
+    """Outputs allocated here on the current stream and written on ``stream``."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, state_out=None,
+                  out=None, initial_state=None, stream=None):
+    """Causal lightning attention whose state decays: ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``,
+    ``o_t = S_t^T q_t``.
+
+    ``q, k, v``: ``[B, N, H, D]`` or packed ``[T, H, D]`` with ``cu_seqlens``, as in
+    ``prefill``; ``g``: their shape without the last axis and their dtype, the log-decay of
+    each token and head (``None``: no decay).  Returns ``o``, or ``(o, state)`` with
+    ``return_state`` or ``state_out`` (final states ``[S, H, D, D]`` fp32).
+    ``initial_state`` as in ``prefill``: ``state_out`` may be that tensor (update in place).
+    """
+    B, H, N, D, S, cu = _gated_shape(q, k, v, g, cu_seqlens)
+    dev, flags = q.device, _flags_for(q.dtype)
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    _need(out, "out", q.dtype, dev)
+    _need_shape(out, "out", q.shape)
+    if any(_overlap(out, t) for t in (q, k, v, g) if t is not None):
+        raise ValueError("out must not overlap an input")
+    st = state_out
+    if return_state and st is None:
+        st = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
+        made.append(st)
+    _need_state(st, "state_out", (S, H, D, D), dev)
+    _need_state(initial_state, "initial_state", (S, H, D, D), dev)
+    if st is not None and initial_state is not None and st.data_ptr() != initial_state.data_ptr() \
+            and _overlap(st, initial_state):
+        raise ValueError("state_out and initial_state overlap without coinciding")
+    cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    n_cu = 0 if cu is None else len(cu) - 1
+    with _on_device(dev, stream):
+        ws, size = _gated_workspace((B, H, N, D), cu_ptr, n_cu, flags, 0, dev, stream)
+        rc = lib().la_gated_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr, n_cu,
+                                    flags, _ptr(initial_state), _ptr(st), _ptr(ws), size,
+                                    _stream_ptr(stream))
+        _check("la_gated_prefill", rc)
+        _used_on(stream, *made)
+    return (out, st) if st is not None else out
+
+
+def gated_prefill_backward(q, k, v, g, do, *, cu_seqlens=None, initial_state=None, d_state=None,
+                           stream=None):
+    """Gradients of ``gated_prefill``: ``(dq, dk, dv, dg)`` from ``do``, the gradient of its
+    output, and with ``initial_state`` ``(dq, dk, dv, dg, d_initial_state)``.
+
+    ``d_state`` (``[S, H, D, D]`` fp32): gradient of the final states.  ``dg`` is ``None``
+    where ``g`` is; these are then the gradients of ``prefill`` (without ``rmsnorm``).  The
+    states are recomputed: nothing has to be kept from the forward call.
+    """
+    B, H, N, D, S, cu = _gated_shape(q, k, v, g, cu_seqlens)
+    dev, flags = q.device, _flags_for(q.dtype)
+    _need(do, "do", q.dtype, dev)
+    _need_shape(do, "do", q.shape)
+    _need_state(initial_state, "initial_state", (S, H, D, D), dev)
+    _need_state(d_state, "d_state", (S, H, D, D), dev)
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    dg = None if g is None else torch.empty_like(g)
+    d_init = None if initial_state is None else torch.empty_like(initial_state)
+    cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    n_cu = 0 if cu is None else len(cu) - 1
+    with _on_device(dev, stream):
+        ws, size = _gated_workspace((B, H, N, D), cu_ptr, n_cu, flags, 1, dev, stream)
+        rc = lib().la_gated_prefill_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), B, H, N, D,
+            cu_ptr, n_cu, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init), _ptr(ws), size,
+            _stream_ptr(stream))
+        _check("la_gated_prefill_backward", rc)
+        _used_on(stream, dq, dk, dv, dg, d_init)
+    return (dq, dk, dv, dg) if d_init is None else (dq, dk, dv, dg, d_init)
+
+
+def gated_decode_step(q, k, v, g, state, *, slots=None, out=None, stream=None):
+    """One token per row: ``state = exp(g) state + k v^T`` in place, returns ``o = state^T q``.
+
+    ``q, k, v``: ``[B, H, D]``; ``g``: ``[B, H]`` or ``None`` (no decay); ``state``:
+    ``[num_slots, H, D, D]`` fp32.  ``slots`` (CUDA int32 ``[B]``): the slot of each row's
+    state, row ``b`` itself without it.  A row of slot -1 is padding: its state and its row
+    of ``o`` stay as they are.  A slot outside the pool, or the slot of an earlier row, is
+    skipped too, and ``device_status`` reports it.
+    """
+    _need(q, "q")
+    dev = q.device
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, q.dtype, dev)
+        if t.shape != q.shape:
+            raise ValueError("q, k, v must have one shape")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, D]")
+    B, H, D = q.shape
+    if g is not None:
+        _need(g, "g", q.dtype, dev)
+        _need_shape(g, "g", (B, H))
+    _need(state, "state", torch.float32, dev)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, D, D):
+        raise ValueError("state must be [num_slots, H, D, D]")
+    if slots is None:
+        if state.shape[0] != B:
+            raise ValueError("state must be [B, H, D, D] without slots")
+    else:
+        _need(slots, "slots", torch.int32, dev)
+        _need_shape(slots, "slots", (B,))
+    flags = _flags_for(q.dtype)
+    made = out is None
+    if made:
+        out = torch.empty_like(q)
+    _need(out, "out", q.dtype, dev)
+    _need_shape(out, "out", q.shape)
+    if any(_overlap(out, t) for t in (q, k, v, g, state) if t is not None):
+        raise ValueError("out must not overlap an input or the state")
+    with _on_device(dev, stream):
+        rc = lib().la_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), B, H, D,
+                                        _ptr(slots), state.shape[0], flags, _stream_ptr(stream))
+        _check("la_gated_decode_step", rc)
+        if made:
+            _used_on(stream, out)
     return out
 
 

@@ -3,16 +3,18 @@
 // Host side only: argument validation, the sequence table, TMA tensor maps and
 // kernel launches.  Every step of the computation runs in the kernels of
 // prefill_pair.cuh and prefill_tc.cuh (bf16, tcgen05), prefill_simt.cuh (fp32),
-// chunk_state.cuh and decode.cuh.
+// chunk_state.cuh, decode.cuh and gated.cuh.
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <numeric>
+#include <type_traits>
 #include <vector>
 
 #include "chunk_state.cuh"
 #include "decode.cuh"
+#include "gated.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_pair.cuh"
 #include "prefill_tc.cuh"
@@ -154,6 +156,158 @@ la_status launch_simt(const float *q, const float *k, const float *v, float *o, 
         return LA_ERR_CUDA;
     kern<<<S * H, C::THREADS, C::SMEM_BYTES, stream>>>(q, k, v, o, state, state_in, H, rmsnorm, seqs);
     return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+
+// ------------------------------------------------------------------ gated operators
+using la::GatedTable;
+
+struct GatedPlan {
+    GatedTable tab;
+    bool segmented;
+    int longest;                   // blocks of the longest sequence
+    // workspace offsets (bytes): state snapshots of both directions, segment states, decays
+    size_t snap, dsnap, seg_state, seg_total, bytes;
+};
+
+// The table and the workspace of a call.  A state scan runs one CTA per (segment, head,
+// slice) one block after the other.  A sequence is cut into segments where the longest one
+// would take more than twice the time that the whole call needs on a full GPU: the segments'
+// own end states then come first (the inputs of the scan are read twice).
+la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs, unsigned flags,
+                     bool backward, GatedPlan &pl, long long &T) {
+    int S = 0;
+    GatedTable &t = pl.tab;
+    if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
+    (void)flags;
+    const int C = la::GatedSimt::C, slices = D / la::GatedSimt::VS, resident = 148 * 4, min_seg = 8;
+    t.S = S;
+    t.C = C;
+    long long blocks = 0;
+    pl.longest = 0;
+    for (int r = 0; r < (t.seqs.varlen ? S : 1); ++r) {
+        const int nb = ((t.seqs.varlen ? t.seqs.seq_len[r] : N) + C - 1) / C;
+        pl.longest = std::max(pl.longest, nb);
+        blocks += t.seqs.varlen ? nb : (long long)nb * S;
+    }
+    const long long even = (blocks * H * slices + resident - 1) / resident;
+    const long long seg = std::max<long long>(min_seg, even);
+    pl.segmented = pl.longest > 2 * seg;
+    t.seg_blocks = pl.segmented ? (int)seg : std::max(1, pl.longest);
+    long long nblk = 0, nseg = 0;
+    if (t.seqs.varlen) {
+        for (int r = 0; r < S; ++r) {
+            const int nb = (t.seqs.seq_len[r] + C - 1) / C;
+            t.block0[r] = (int)nblk;
+            t.seg0[r] = (int)nseg;
+            nblk += nb;
+            nseg += std::max(1, (nb + t.seg_blocks - 1) / t.seg_blocks);
+        }
+        t.block0[S] = (int)nblk;
+        t.seg0[S] = (int)nseg;
+        t.blocks_per_seq = t.segs_per_seq = 0;
+    } else {
+        t.blocks_per_seq = pl.longest;
+        t.segs_per_seq = std::max(1, (pl.longest + t.seg_blocks - 1) / t.seg_blocks);
+        nblk = (long long)S * t.blocks_per_seq;
+        nseg = (long long)S * t.segs_per_seq;
+    }
+    if (T >= (1ll << 31) || nblk * H >= (1ll << 31) || nseg * H * slices >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
+    t.blocks = (int)nblk;
+    t.segs = (int)nseg;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += (n + 255) & ~(size_t)255;
+        return o;
+    };
+    const size_t state = (size_t)D * D * 4;
+    pl.snap = take((size_t)nblk * H * state);
+    pl.dsnap = take(backward ? (size_t)nblk * H * state : 0);
+    pl.seg_state = take(pl.segmented ? (size_t)nseg * H * state : 0);
+    pl.seg_total = take(pl.segmented ? (size_t)nseg * H * 4 : 0);
+    pl.bytes = at;
+    return LA_OK;
+}
+
+la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
+
+// State scan of one direction: snapshots per block, the final state where wanted.
+template <int D, typename T, bool REV>
+la_status gated_states_simt(const T *a, const T *b, const T *g, const float *initial, float *snap, float *fin,
+                            int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+    auto kern = la::gated_state_simt_kernel<D, T, REV>;
+    const unsigned grid = (unsigned)(pl.tab.segs * H * (D / la::GatedSimt::VS));
+    float *seg_state = nullptr, *seg_total = nullptr;
+    if (pl.segmented) {
+        seg_state = reinterpret_cast<float *>(ws + pl.seg_state);
+        seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
+        kern<<<grid, la::GatedSimt::THREADS, 0, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
+                                                         nullptr, nullptr, H, pl.tab);
+        if (la_status st = launched(); st != LA_OK) return st;
+        la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
+            reinterpret_cast<float4 *>(seg_state), seg_total, reinterpret_cast<const float4 *>(initial), H,
+            D * D / 4, REV ? 1 : 0, pl.tab);
+        if (la_status st = launched(); st != LA_OK) return st;
+    }
+    kern<<<grid, la::GatedSimt::THREADS, 0, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
+                                                     H, pl.tab);
+    return launched();
+}
+
+template <int D, typename T>
+la_status gated_prefill_simt(const T *q, const T *k, const T *v, const T *g, T *o, const float *state_in,
+                             float *state_out, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+    float *snap = nullptr;
+    if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
+    if (snap != nullptr || state_out != nullptr)
+        if (la_status st = gated_states_simt<D, T, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
+            st != LA_OK)
+            return st;
+    if (pl.tab.blocks == 0) return LA_OK;
+    auto kern = la::gated_prefill_simt_kernel<D, T>;
+    constexpr int smem = la::GatedSimtTiles<D>::FWD_BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return LA_ERR_CUDA;
+    kern<<<(unsigned)(pl.tab.blocks * H), la::GatedSimt::THREADS, smem, stream>>>(q, k, v, g, o, snap, H, pl.tab);
+    return launched();
+}
+
+template <int D, typename T>
+la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, const T *dout, T *dq, T *dk, T *dv,
+                              T *dg, const float *state_in, const float *d_state, float *d_state_in, int H,
+                              const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+    float *snap = nullptr, *dsnap = nullptr;
+    if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
+    if (pl.longest > 1 || d_state != nullptr) dsnap = reinterpret_cast<float *>(ws + pl.dsnap);
+    if (snap != nullptr)
+        if (la_status st = gated_states_simt<D, T, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, stream);
+            st != LA_OK)
+            return st;
+    if (dsnap != nullptr || d_state_in != nullptr)
+        if (la_status st = gated_states_simt<D, T, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, stream);
+            st != LA_OK)
+            return st;
+    if (pl.tab.blocks == 0) return LA_OK;
+    auto kern = la::gated_backward_simt_kernel<D, T>;
+    constexpr int smem = la::GatedSimtTiles<D>::BWD_BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return LA_ERR_CUDA;
+    kern<<<(unsigned)(pl.tab.blocks * H), la::GatedSimt::THREADS, smem, stream>>>(q, k, v, g, dout, dq, dk, dv, dg,
+                                                                                 snap, dsnap, H, pl.tab);
+    return launched();
+}
+
+// Checks that the gated sequence operators share.
+la_status check_gated(int B, int H, int N, int D, unsigned flags) {
+    if (flags & ~(unsigned)LA_BF16) return LA_ERR_INVALID_ARG;
+    if (H < 1 || N < 0 || B < 1) return LA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+bool aligned_gate(const void *p, unsigned flags) {
+    return (reinterpret_cast<uintptr_t>(p) & ((flags & LA_BF16) ? 1u : 3u)) == 0;
 }
 
 }  // namespace
@@ -426,6 +580,110 @@ la_status la_state_out(const float *state_ws, float *state_dst, int S, int H, in
         reinterpret_cast<const float4 *>(state_ws), reinterpret_cast<float4 *>(state_dst),
         seq_to_slot, H, D * D / 4, num_slots);
     return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_gated_workspace(int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs, unsigned flags,
+                             int backward, unsigned long long *bytes) {
+    if (bytes == nullptr) return LA_ERR_INVALID_ARG;
+    if (la_status st = check_gated(B, H, N, D, flags); st != LA_OK) return st;
+    GatedPlan pl;
+    long long T = 0;
+    if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, backward != 0, pl, T); st != LA_OK)
+        return st;
+    *bytes = pl.bytes;
+    return LA_OK;
+}
+
+la_status la_gated_prefill(const void *q, const void *k, const void *v, const void *g, void *o, int B, int H, int N,
+                           int D, const int32_t *cu_seqlens, int num_seqs, unsigned flags, const float *state_in,
+                           float *state_out, void *workspace, unsigned long long workspace_bytes, void *stream_) {
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (la_status st = check_gated(B, H, N, D, flags); st != LA_OK) return st;
+    if (N > 0 && (!q || !k || !v || !o)) return LA_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, (const void *)o, (const void *)state_in, (const void *)state_out,
+                          (const void *)workspace})
+        if (!aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!aligned_gate(g, flags)) return LA_ERR_INVALID_ARG;
+    GatedPlan pl;
+    long long T = 0;
+    if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, false, pl, T); st != LA_OK) return st;
+    if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    auto run = [&](auto *x) -> la_status {
+        using E = std::remove_pointer_t<decltype(x)>;
+        const E *qe = static_cast<const E *>(q), *ke = static_cast<const E *>(k), *ve = static_cast<const E *>(v),
+                *ge = static_cast<const E *>(g);
+        E *oe = static_cast<E *>(o);
+        if (D == 128) return gated_prefill_simt<128>(qe, ke, ve, ge, oe, state_in, state_out, H, pl, ws, stream);
+        return gated_prefill_simt<64>(qe, ke, ve, ge, oe, state_in, state_out, H, pl, ws, stream);
+    };
+    if (flags & LA_BF16) return run(static_cast<__nv_bfloat16 *>(nullptr));
+    return run(static_cast<float *>(nullptr));
+}
+
+la_status la_gated_prefill_backward(const void *q, const void *k, const void *v, const void *g, const void *dout,
+                                    void *dq, void *dk, void *dv, void *dg, int B, int H, int N, int D,
+                                    const int32_t *cu_seqlens, int num_seqs, unsigned flags, const float *state_in,
+                                    const float *d_state, float *d_state_in, void *workspace,
+                                    unsigned long long workspace_bytes, void *stream_) {
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (la_status st = check_gated(B, H, N, D, flags); st != LA_OK) return st;
+    if (N > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv)) return LA_ERR_INVALID_ARG;
+    if (dg != nullptr && g == nullptr) return LA_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, dout, (const void *)dq, (const void *)dk, (const void *)dv,
+                          (const void *)state_in, (const void *)d_state, (const void *)d_state_in,
+                          (const void *)workspace})
+        if (!aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!aligned_gate(g, flags) || !aligned_gate(dg, flags)) return LA_ERR_INVALID_ARG;
+    GatedPlan pl;
+    long long T = 0;
+    if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, true, pl, T); st != LA_OK) return st;
+    if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    auto run = [&](auto *x) -> la_status {
+        using E = std::remove_pointer_t<decltype(x)>;
+        const E *qe = static_cast<const E *>(q), *ke = static_cast<const E *>(k), *ve = static_cast<const E *>(v),
+                *ge = static_cast<const E *>(g), *de = static_cast<const E *>(dout);
+        E *dqe = static_cast<E *>(dq), *dke = static_cast<E *>(dk), *dve = static_cast<E *>(dv),
+          *dge = static_cast<E *>(dg);
+        if (D == 128)
+            return gated_backward_simt<128>(qe, ke, ve, ge, de, dqe, dke, dve, dge, state_in, d_state, d_state_in, H,
+                                            pl, ws, stream);
+        return gated_backward_simt<64>(qe, ke, ve, ge, de, dqe, dke, dve, dge, state_in, d_state, d_state_in, H, pl,
+                                       ws, stream);
+    };
+    if (flags & LA_BF16) return run(static_cast<__nv_bfloat16 *>(nullptr));
+    return run(static_cast<float *>(nullptr));
+}
+
+la_status la_gated_decode_step(const void *q, const void *k, const void *v, const void *g, float *state, void *o,
+                               int B, int H, int D, const int32_t *slots, int num_slots, unsigned flags,
+                               void *stream_) {
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (flags & ~(unsigned)LA_BF16) return LA_ERR_INVALID_ARG;
+    if (B < 0 || H < 1 || num_slots < 0) return LA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    if (!q || !k || !v || !o || !state) return LA_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, (const void *)o, (const void *)state})
+        if (!aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!aligned_gate(g, flags) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return LA_ERR_INVALID_ARG;
+    if (slots == nullptr && num_slots < B) return LA_ERR_INVALID_ARG;
+    if ((long long)B * H >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)(B * H);
+    auto run = [&](auto *x) {
+        using E = std::remove_pointer_t<decltype(x)>;
+        const E *qe = static_cast<const E *>(q), *ke = static_cast<const E *>(k), *ve = static_cast<const E *>(v),
+                *ge = static_cast<const E *>(g);
+        E *oe = static_cast<E *>(o);
+        if (D == 128)
+            la::gated_decode_kernel<128, E><<<grid, 256, 0, stream>>>(qe, ke, ve, ge, state, oe, H, slots, num_slots);
+        else
+            la::gated_decode_kernel<64, E><<<grid, 256, 0, stream>>>(qe, ke, ve, ge, state, oe, H, slots, num_slots);
+        return launched();
+    };
+    if (flags & LA_BF16) return run(static_cast<__nv_bfloat16 *>(nullptr));
+    return run(static_cast<float *>(nullptr));
 }
 
 la_status la_get_device_status(void *stream_) {
