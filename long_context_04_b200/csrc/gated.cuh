@@ -87,9 +87,10 @@ struct GatedTable {
     }
 };
 
-// A log-decay as the kernels use it.  e^{-1000} is 0 in fp32, as e^{-inf} is, and a finite
-// bound keeps differences of sums defined; a NaN stays one.
-__device__ __forceinline__ float clamp_gate(float g) { return g < -1000.f ? -1000.f : g; }
+// A log-decay as the kernels use it.  e^{-110} is 0 in fp32, as e^{-inf} is; a finite bound
+// keeps differences of sums defined, and a small one keeps them exact: 128 such tokens sum to
+// 2^14, whose rounding is 2^-10.  A NaN stays one.
+__device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.f : g; }
 
 // out = start states of a (sequence, head)'s segments from their own end states, in order:
 //     X_0 = initial, X_{s+1} = e^{total_s} X_s + local_s;   seg_state[s] <- X_s.

@@ -3,7 +3,7 @@
 // Host side only: argument validation, the sequence table, TMA tensor maps and
 // kernel launches.  Every step of the computation runs in the kernels of
 // prefill_pair.cuh and prefill_tc.cuh (bf16, tcgen05), prefill_simt.cuh (fp32),
-// chunk_state.cuh, decode.cuh and gated.cuh.
+// chunk_state.cuh, decode.cuh and the gated*.cuh files.
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
@@ -15,6 +15,8 @@
 #include "chunk_state.cuh"
 #include "decode.cuh"
 #include "gated.cuh"
+#include "gated_backward_tc.cuh"
+#include "gated_state_tc.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_pair.cuh"
 #include "prefill_tc.cuh"
@@ -25,6 +27,7 @@ namespace {
 using la::PrefillTcParams;
 using la::SeqTable;
 
+constexpr int kSMs = 148;
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s per wait
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -166,8 +169,9 @@ struct GatedPlan {
     GatedTable tab;
     bool segmented;
     int longest;                   // blocks of the longest sequence
-    // workspace offsets (bytes): state snapshots of both directions, segment states, decays
-    size_t snap, dsnap, seg_state, seg_total, bytes;
+    // workspace offsets (bytes): state snapshots of both directions, the parts of <dS, S>,
+    // segment states, their decays
+    size_t snap, dsnap, through, seg_state, seg_total, bytes;
 };
 
 // The table and the workspace of a call.  A state scan runs one CTA per (segment, head,
@@ -179,8 +183,11 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     int S = 0;
     GatedTable &t = pl.tab;
     if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
-    (void)flags;
-    const int C = la::GatedSimt::C, slices = D / la::GatedSimt::VS, resident = 148 * 4, min_seg = 8;
+    // tensor-core scan: 128-token blocks, bf16 snapshots, one CTA per SM; CUDA-core scan:
+    // 64-token blocks, fp32 snapshots, four CTAs per SM
+    const bool tc = (flags & LA_BF16) && backward;
+    const int C = tc ? 128 : la::GatedSimt::C, slices = tc ? D / 64 : D / la::GatedSimt::VS;
+    const int resident = tc ? kSMs : 4 * kSMs, min_seg = 8;
     t.S = S;
     t.C = C;
     long long blocks = 0;
@@ -212,7 +219,8 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         nblk = (long long)S * t.blocks_per_seq;
         nseg = (long long)S * t.segs_per_seq;
     }
-    if (T >= (1ll << 31) || nblk * H >= (1ll << 31) || nseg * H * slices >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
+    // (the snapshots' rows, nblk * H * D, are coordinates of a tensor map)
+    if (T >= (1ll << 31) || nblk * H * D >= (1ll << 31) || nseg * H * slices >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
     t.blocks = (int)nblk;
     t.segs = (int)nseg;
     size_t at = 0;
@@ -221,9 +229,10 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         at += (n + 255) & ~(size_t)255;
         return o;
     };
-    const size_t state = (size_t)D * D * 4;
-    pl.snap = take((size_t)nblk * H * state);
-    pl.dsnap = take(backward ? (size_t)nblk * H * state : 0);
+    const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
+    pl.snap = take((size_t)nblk * H * shot);
+    pl.dsnap = take(backward ? (size_t)nblk * H * shot : 0);
+    pl.through = take(tc ? (size_t)nblk * H * 4 * slices * 4 : 0);
     pl.seg_state = take(pl.segmented ? (size_t)nseg * H * state : 0);
     pl.seg_total = take(pl.segmented ? (size_t)nseg * H * 4 : 0);
     pl.bytes = at;
@@ -295,6 +304,94 @@ la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, co
         return LA_ERR_CUDA;
     kern<<<(unsigned)(pl.tab.blocks * H), la::GatedSimt::THREADS, smem, stream>>>(q, k, v, g, dout, dq, dk, dv, dg,
                                                                                  snap, dsnap, H, pl.tab);
+    return launched();
+}
+
+// The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
+template <int D, bool REV>
+la_status gated_states_tc(const void *a, const void *b, const void *g, const float *initial, void *snap,
+                          const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
+                          uint8_t *ws, cudaStream_t stream) {
+    using C = la::GatedStateCfg<D>;
+    using bf = __nv_bfloat16;
+    auto kern = la::gated_state_tc_kernel<D, REV>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+        return LA_ERR_CUDA;
+    la::GatedStateParams p;
+    std::memset(&p, 0, sizeof p);
+    if (T > 0 && (!make_map(&p.tmap_a, a, T, H, D, C::C) || !make_map(&p.tmap_b, b, T, H, D, C::C))) return LA_ERR_CUDA;
+    p.g = static_cast<const bf *>(g);
+    p.H = H;
+    p.timeout_ns = kWaitLimitNs;
+    p.tab = pl.tab;
+    const unsigned grid = (unsigned)(pl.tab.segs * H * C::NVS);
+    if (pl.segmented) {
+        p.seg_out = reinterpret_cast<float *>(ws + pl.seg_state);
+        p.seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
+        kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+        if (la_status st = launched(); st != LA_OK) return st;
+        la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
+            reinterpret_cast<float4 *>(p.seg_out), p.seg_total, reinterpret_cast<const float4 *>(initial), H,
+            D * D / 4, REV ? 1 : 0, pl.tab);
+        if (la_status st = launched(); st != LA_OK) return st;
+        p.seg_in = p.seg_out;
+        p.seg_out = p.seg_total = nullptr;
+    }
+    p.initial = initial;
+    p.fin = fin;
+    p.snap = static_cast<bf *>(snap);
+    p.other = static_cast<const bf *>(other);
+    p.through = through;
+    kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    return launched();
+}
+
+template <int D>
+la_status gated_backward_tc(const void *q, const void *k, const void *v, const void *g, const void *dout, void *dq,
+                            void *dk, void *dv, void *dg, const float *state_in, const float *d_state,
+                            float *d_state_in, int H, long long T, const GatedPlan &pl, uint8_t *ws,
+                            cudaStream_t stream) {
+    using C = la::GatedBackwardCfg<D>;
+    using bf = __nv_bfloat16;
+    void *snap = nullptr, *dsnap = nullptr;
+    float *through = nullptr;
+    if (pl.longest > 1 || state_in != nullptr) snap = ws + pl.snap;
+    if (pl.longest > 1 || d_state != nullptr) dsnap = ws + pl.dsnap;
+    if (snap != nullptr && dsnap != nullptr && dg != nullptr) through = reinterpret_cast<float *>(ws + pl.through);
+    if (snap != nullptr && pl.tab.blocks > 0)
+        if (la_status st = gated_states_tc<D, false>(k, v, g, state_in, snap, nullptr, nullptr, nullptr, H, T, pl, ws,
+                                                     stream);
+            st != LA_OK)
+            return st;
+    if (dsnap != nullptr || d_state_in != nullptr)
+        if (la_status st = gated_states_tc<D, true>(q, dout, g, d_state, dsnap, snap, through, d_state_in, H, T, pl,
+                                                    ws, stream);
+            st != LA_OK)
+            return st;
+    if (pl.tab.blocks == 0) return LA_OK;
+    la::GatedBackwardParams p;
+    std::memset(&p, 0, sizeof p);
+    const long long rows = (long long)pl.tab.blocks * H * D;
+    if (!make_map(&p.tmap_q, q, T, H, D, C::C) || !make_map(&p.tmap_k, k, T, H, D, C::C) ||
+        !make_map(&p.tmap_v, v, T, H, D, C::C) || !make_map(&p.tmap_do, dout, T, H, D, C::C) ||
+        (snap != nullptr && !make_map(&p.tmap_s, snap, rows, 1, D, D)) ||
+        (dsnap != nullptr && !make_map(&p.tmap_ds, dsnap, rows, 1, D, D)))
+        return LA_ERR_CUDA;
+    p.g = static_cast<const bf *>(g);
+    p.through = through;
+    p.dq = static_cast<bf *>(dq);
+    p.dk = static_cast<bf *>(dk);
+    p.dv = static_cast<bf *>(dv);
+    p.dg = static_cast<bf *>(dg);
+    p.H = H;
+    p.have_s = snap != nullptr;
+    p.have_ds = dsnap != nullptr;
+    p.timeout_ns = kWaitLimitNs;
+    p.tab = pl.tab;
+    auto kern = la::gated_backward_tc_kernel<D>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+        return LA_ERR_CUDA;
+    kern<<<(unsigned)std::min(kSMs, pl.tab.blocks * H), C::THREADS, C::SMEM_BYTES, stream>>>(p);
     return launched();
 }
 
@@ -640,20 +737,23 @@ la_status la_gated_prefill_backward(const void *q, const void *k, const void *v,
     if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, true, pl, T); st != LA_OK) return st;
     if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    auto run = [&](auto *x) -> la_status {
-        using E = std::remove_pointer_t<decltype(x)>;
-        const E *qe = static_cast<const E *>(q), *ke = static_cast<const E *>(k), *ve = static_cast<const E *>(v),
-                *ge = static_cast<const E *>(g), *de = static_cast<const E *>(dout);
-        E *dqe = static_cast<E *>(dq), *dke = static_cast<E *>(dk), *dve = static_cast<E *>(dv),
-          *dge = static_cast<E *>(dg);
+    if (flags & LA_BF16) {
         if (D == 128)
-            return gated_backward_simt<128>(qe, ke, ve, ge, de, dqe, dke, dve, dge, state_in, d_state, d_state_in, H,
-                                            pl, ws, stream);
-        return gated_backward_simt<64>(qe, ke, ve, ge, de, dqe, dke, dve, dge, state_in, d_state, d_state_in, H, pl,
-                                       ws, stream);
-    };
-    if (flags & LA_BF16) return run(static_cast<__nv_bfloat16 *>(nullptr));
-    return run(static_cast<float *>(nullptr));
+            return gated_backward_tc<128>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
+                                          stream);
+        return gated_backward_tc<64>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
+                                     stream);
+    }
+    const float *qf = static_cast<const float *>(q), *kf = static_cast<const float *>(k),
+                *vf = static_cast<const float *>(v), *gf = static_cast<const float *>(g),
+                *df = static_cast<const float *>(dout);
+    float *dqf = static_cast<float *>(dq), *dkf = static_cast<float *>(dk), *dvf = static_cast<float *>(dv),
+          *dgf = static_cast<float *>(dg);
+    if (D == 128)
+        return gated_backward_simt<128>(qf, kf, vf, gf, df, dqf, dkf, dvf, dgf, state_in, d_state, d_state_in, H, pl, ws,
+                                        stream);
+    return gated_backward_simt<64>(qf, kf, vf, gf, df, dqf, dkf, dvf, dgf, state_in, d_state, d_state_in, H, pl, ws,
+                                   stream);
 }
 
 la_status la_gated_decode_step(const void *q, const void *k, const void *v, const void *g, float *state, void *o,
