@@ -89,12 +89,6 @@ __device__ __forceinline__ float warp_column_sums(float (&w)[32]) {
     return w[0];
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <int D>
 __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     gated_backward_tc_kernel(const __grid_constant__ GatedBackwardParams p) {

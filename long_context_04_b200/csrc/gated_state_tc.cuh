@@ -145,6 +145,12 @@ __device__ __forceinline__ void split3(const uint4 &raw, float w, bool keep, uin
     p2 = make_uint4(out[2][0], out[2][1], out[2][2], out[2][3]);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 r;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"

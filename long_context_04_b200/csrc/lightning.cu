@@ -16,6 +16,7 @@
 #include "decode.cuh"
 #include "gated.cuh"
 #include "gated_backward_tc.cuh"
+#include "gated_prefill_tc.cuh"
 #include "gated_state_tc.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_pair.cuh"
@@ -183,9 +184,10 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     int S = 0;
     GatedTable &t = pl.tab;
     if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
-    // tensor-core scan: 128-token blocks, bf16 snapshots, one CTA per SM; CUDA-core scan:
-    // 64-token blocks, fp32 snapshots, four CTAs per SM
-    const bool tc = (flags & LA_BF16) && backward;
+    // tensor cores: 128-token blocks, one CTA per SM, bf16 snapshots (of the backward pass
+    // alone: the prefill kernel keeps its state on chip); CUDA cores: 64-token blocks, four
+    // CTAs per SM, fp32 snapshots
+    const bool tc = (flags & LA_BF16) != 0;
     const int C = tc ? 128 : la::GatedSimt::C, slices = tc ? D / 64 : D / la::GatedSimt::VS;
     const int resident = tc ? kSMs : 4 * kSMs, min_seg = 8;
     t.S = S;
@@ -230,9 +232,9 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         return o;
     };
     const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
-    pl.snap = take((size_t)nblk * H * shot);
+    pl.snap = take(tc && !backward ? 0 : (size_t)nblk * H * shot);
     pl.dsnap = take(backward ? (size_t)nblk * H * shot : 0);
-    pl.through = take(tc ? (size_t)nblk * H * 4 * slices * 4 : 0);
+    pl.through = take(tc && backward ? (size_t)nblk * H * 4 * slices * 4 : 0);
     pl.seg_state = take(pl.segmented ? (size_t)nseg * H * state : 0);
     pl.seg_total = take(pl.segmented ? (size_t)nseg * H * 4 : 0);
     pl.bytes = at;
@@ -273,7 +275,6 @@ la_status gated_prefill_simt(const T *q, const T *k, const T *v, const T *g, T *
         if (la_status st = gated_states_simt<D, T, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
             st != LA_OK)
             return st;
-    if (pl.tab.blocks == 0) return LA_OK;
     auto kern = la::gated_prefill_simt_kernel<D, T>;
     constexpr int smem = la::GatedSimtTiles<D>::FWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -297,7 +298,6 @@ la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, co
         if (la_status st = gated_states_simt<D, T, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, stream);
             st != LA_OK)
             return st;
-    if (pl.tab.blocks == 0) return LA_OK;
     auto kern = la::gated_backward_simt_kernel<D, T>;
     constexpr int smem = la::GatedSimtTiles<D>::BWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -309,40 +309,108 @@ la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, co
 
 // The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
 template <int D, bool REV>
-la_status gated_states_tc(const void *a, const void *b, const void *g, const float *initial, void *snap,
-                          const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
-                          uint8_t *ws, cudaStream_t stream) {
+la_status launch_gated_states(const la::GatedStateParams &p, cudaStream_t stream) {
     using C = la::GatedStateCfg<D>;
-    using bf = __nv_bfloat16;
     auto kern = la::gated_state_tc_kernel<D, REV>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
-    la::GatedStateParams p;
+    kern<<<(unsigned)(p.tab.segs * p.H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    return launched();
+}
+
+template <int D>
+bool fill_gated_states(la::GatedStateParams &p, const void *a, const void *b, const void *g, int H, long long T,
+                       const GatedPlan &pl) {
     std::memset(&p, 0, sizeof p);
-    if (T > 0 && (!make_map(&p.tmap_a, a, T, H, D, C::C) || !make_map(&p.tmap_b, b, T, H, D, C::C))) return LA_ERR_CUDA;
-    p.g = static_cast<const bf *>(g);
+    p.g = static_cast<const __nv_bfloat16 *>(g);
     p.H = H;
     p.timeout_ns = kWaitLimitNs;
     p.tab = pl.tab;
-    const unsigned grid = (unsigned)(pl.tab.segs * H * C::NVS);
+    return make_map(&p.tmap_a, a, T, H, D, la::GatedStateCfg<D>::C) &&
+           make_map(&p.tmap_b, b, T, H, D, la::GatedStateCfg<D>::C);
+}
+
+// The start states of a segmented call's segments (in place of their own end states).
+template <int D, bool REV>
+la_status gated_seg_states_tc(la::GatedStateParams p, const float *initial, const GatedPlan &pl, uint8_t *ws,
+                              cudaStream_t stream, float *&seg_in) {
+    p.seg_out = seg_in = reinterpret_cast<float *>(ws + pl.seg_state);
+    p.seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
+    if (la_status st = launch_gated_states<D, REV>(p, stream); st != LA_OK) return st;
+    la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * p.H), D * D / 1024), 256, 0, stream>>>(
+        reinterpret_cast<float4 *>(p.seg_out), p.seg_total, reinterpret_cast<const float4 *>(initial), p.H,
+        D * D / 4, REV ? 1 : 0, pl.tab);
+    return launched();
+}
+
+template <int D, bool REV>
+la_status gated_states_tc(const void *a, const void *b, const void *g, const float *initial, void *snap,
+                          const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
+                          uint8_t *ws, cudaStream_t stream) {
+    using bf = __nv_bfloat16;
+    la::GatedStateParams p;
+    if (!fill_gated_states<D>(p, a, b, g, H, T, pl)) return LA_ERR_CUDA;
     if (pl.segmented) {
-        p.seg_out = reinterpret_cast<float *>(ws + pl.seg_state);
-        p.seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
-        kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-        if (la_status st = launched(); st != LA_OK) return st;
-        la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
-            reinterpret_cast<float4 *>(p.seg_out), p.seg_total, reinterpret_cast<const float4 *>(initial), H,
-            D * D / 4, REV ? 1 : 0, pl.tab);
-        if (la_status st = launched(); st != LA_OK) return st;
-        p.seg_in = p.seg_out;
-        p.seg_out = p.seg_total = nullptr;
+        float *seg_in = nullptr;
+        if (la_status st = gated_seg_states_tc<D, REV>(p, initial, pl, ws, stream, seg_in); st != LA_OK) return st;
+        p.seg_in = seg_in;
     }
     p.initial = initial;
     p.fin = fin;
     p.snap = static_cast<bf *>(snap);
     p.other = static_cast<const bf *>(other);
     p.through = through;
-    kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    return launch_gated_states<D, REV>(p, stream);
+}
+
+// Final states of sequences without tokens: their initial states.
+la_status gated_no_tokens(const float *initial, float *fin, int S, int H, int D, cudaStream_t stream) {
+    if (fin == nullptr || fin == initial) return LA_OK;
+    if (initial == nullptr)
+        la::state_zero_kernel<<<(unsigned)(S * H), 256, 0, stream>>>(reinterpret_cast<float4 *>(fin), D * D / 4);
+    else
+        la::state_copy_kernel<<<(unsigned)(S * H), 256, 0, stream>>>(reinterpret_cast<const float4 *>(initial),
+                                                                     reinterpret_cast<float4 *>(fin), nullptr, H,
+                                                                     D * D / 4, S);
+    return launched();
+}
+
+template <int D>
+la_status gated_prefill_tc(const void *q, const void *k, const void *v, const void *g, void *o, const float *state_in,
+                           float *state_out, int H, long long T, const GatedPlan &pl, uint8_t *ws,
+                           cudaStream_t stream) {
+    using C = la::GatedPrefillCfg<D>;
+    auto kern = la::gated_prefill_tc_kernel<D>;
+    // The warpgroups trade registers (setmaxnreg): the block has to start with what their shares
+    // add up to, or a group would wait for registers that nobody gives back.
+    static const bool fits = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
+               at.numRegs * 5 >= C::R_MISC + C::R_KV + C::R_P + C::R_O + C::R_V;
+    }();
+    if (!fits) return LA_ERR_CUDA;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+        return LA_ERR_CUDA;
+    la::GatedPrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    if (!make_map(&p.tmap_q, q, T, H, D, C::C) || !make_map(&p.tmap_k, k, T, H, D, C::C) ||
+        !make_map(&p.tmap_v, v, T, H, D, C::C))
+        return LA_ERR_CUDA;
+    if (pl.segmented) {
+        la::GatedStateParams sp;
+        float *seg_in = nullptr;
+        if (!fill_gated_states<D>(sp, k, v, g, H, T, pl)) return LA_ERR_CUDA;
+        if (la_status st = gated_seg_states_tc<D, false>(sp, state_in, pl, ws, stream, seg_in); st != LA_OK) return st;
+        p.seg_in = seg_in;
+    }
+    p.g = static_cast<const __nv_bfloat16 *>(g);
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.initial = state_in;
+    p.fin = state_out;
+    p.H = H;
+    p.timeout_ns = kWaitLimitNs;
+    p.tab = pl.tab;
+    kern<<<(unsigned)(pl.tab.segs * H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
     return launched();
 }
 
@@ -358,7 +426,7 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
     if (pl.longest > 1 || state_in != nullptr) snap = ws + pl.snap;
     if (pl.longest > 1 || d_state != nullptr) dsnap = ws + pl.dsnap;
     if (snap != nullptr && dsnap != nullptr && dg != nullptr) through = reinterpret_cast<float *>(ws + pl.through);
-    if (snap != nullptr && pl.tab.blocks > 0)
+    if (snap != nullptr)
         if (la_status st = gated_states_tc<D, false>(k, v, g, state_in, snap, nullptr, nullptr, nullptr, H, T, pl, ws,
                                                      stream);
             st != LA_OK)
@@ -368,7 +436,6 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
                                                     ws, stream);
             st != LA_OK)
             return st;
-    if (pl.tab.blocks == 0) return LA_OK;
     la::GatedBackwardParams p;
     std::memset(&p, 0, sizeof p);
     const long long rows = (long long)pl.tab.blocks * H * D;
@@ -706,16 +773,16 @@ la_status la_gated_prefill(const void *q, const void *k, const void *v, const vo
     if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, false, pl, T); st != LA_OK) return st;
     if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    auto run = [&](auto *x) -> la_status {
-        using E = std::remove_pointer_t<decltype(x)>;
-        const E *qe = static_cast<const E *>(q), *ke = static_cast<const E *>(k), *ve = static_cast<const E *>(v),
-                *ge = static_cast<const E *>(g);
-        E *oe = static_cast<E *>(o);
-        if (D == 128) return gated_prefill_simt<128>(qe, ke, ve, ge, oe, state_in, state_out, H, pl, ws, stream);
-        return gated_prefill_simt<64>(qe, ke, ve, ge, oe, state_in, state_out, H, pl, ws, stream);
-    };
-    if (flags & LA_BF16) return run(static_cast<__nv_bfloat16 *>(nullptr));
-    return run(static_cast<float *>(nullptr));
+    if (T == 0) return gated_no_tokens(state_in, state_out, pl.tab.S, H, D, stream);
+    if (flags & LA_BF16) {
+        if (D == 128) return gated_prefill_tc<128>(q, k, v, g, o, state_in, state_out, H, T, pl, ws, stream);
+        return gated_prefill_tc<64>(q, k, v, g, o, state_in, state_out, H, T, pl, ws, stream);
+    }
+    const float *qf = static_cast<const float *>(q), *kf = static_cast<const float *>(k),
+                *vf = static_cast<const float *>(v), *gf = static_cast<const float *>(g);
+    float *of = static_cast<float *>(o);
+    if (D == 128) return gated_prefill_simt<128>(qf, kf, vf, gf, of, state_in, state_out, H, pl, ws, stream);
+    return gated_prefill_simt<64>(qf, kf, vf, gf, of, state_in, state_out, H, pl, ws, stream);
 }
 
 la_status la_gated_prefill_backward(const void *q, const void *k, const void *v, const void *g, const void *dout,
@@ -737,6 +804,7 @@ la_status la_gated_prefill_backward(const void *q, const void *k, const void *v,
     if (la_status st = plan_gated(B, H, N, D, cu_seqlens, num_seqs, flags, true, pl, T); st != LA_OK) return st;
     if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (T == 0) return gated_no_tokens(d_state, d_state_in, pl.tab.S, H, D, stream);
     if (flags & LA_BF16) {
         if (D == 128)
             return gated_backward_tc<128>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
