@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         record_fault(DEV_TIMEOUT);
     };
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tlimit)) != 0;
+        return warp_wait(bar, parity, abort_flag, tlimit);
     };
     uint32_t load_phase = 1;      // of thread 0: the phase of its last loads
     auto load = [&](int x) {      // thread 0: the tiles of tile x
@@ -189,8 +189,10 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         }
         if (warp == 0) {
             // ------------------------------------------------------------ gates, loads, dg
+            uint32_t raw[4];
             float gate[4], sums[4], aft[4];
-            load_gates4(gate, p.g, row0, nv, p.H, h);
+            fetch_gates4(raw, p.g, row0, nv, p.H, h);
+            widen_gates4(gate, raw);
             prefix_gates4(gate, sums);
             suffix_gates4(gate, aft);
             float part = 0.f;

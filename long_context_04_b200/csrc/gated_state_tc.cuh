@@ -50,8 +50,8 @@ struct GatedStateCfg {
     static constexpr int LOADED = (DB + 1) * BOX;
     static constexpr int NST = 2;
     static constexpr int SCALERS = 6;               // warps (12 in all: 168 registers a thread)
-    static constexpr int OFF_W = NST * STAGE;       // decays, 128 floats per scaling warp
-    static constexpr int OFF_MISC = OFF_W + SCALERS * C * 4;
+    static constexpr int OFF_G = NST * STAGE;       // gate sums, two blocks
+    static constexpr int OFF_MISC = OFF_G + 2 * C * 4;
     static constexpr int SMEM_USED = 1024 + OFF_MISC + 1024;
     // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
     static constexpr int SMEM_BYTES = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
@@ -66,20 +66,44 @@ struct GatedStateCfg {
 struct GatedStateMisc {
     uint64_t full[2], ready[2], empty[2];  // tiles landed, scaled, released
     uint64_t acc_full[2], acc_free[2];
+    uint64_t gates_ready[2], gates_free[2];
     uint64_t done;
+    float sum[2];          // log-decay of a block, times log2(e)
     uint32_t tmem_base;
     int abort_flag;
 };
 
-// The log-decays of tokens 4 * lane .. 4 * lane + 3 of a block (0 behind the sequence).
-__device__ __forceinline__ void load_gates4(float (&x)[4], const __nv_bfloat16 *__restrict__ g, int row0,
-                                            int nv, int H, int h) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = 4 * lane + e;
-        x[e] = g != nullptr && i < nv ? clamp_gate(__bfloat162float(g[(size_t)(row0 + i) * H + h])) : 0.f;
+// A wait of a whole warp for a phase: true once every lane has seen it complete, false after
+// `limit_ns` or once another warp gave up.  Written for few instructions: these kernels run
+// six roles at once, whose code has to fit the instruction cache together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const volatile int *abort_flag,
+                                          uint64_t limit_ns) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t0 > limit_ns)) return false;
     }
+    return true;
+}
+
+// The log-decays of tokens 4 * lane .. 4 * lane + 3 of a block, as they lie in memory (0
+// behind the sequence), and as the kernels use them.  Fetched a block ahead: the widening
+// is kept behind what the caller waits for in between, or the loads' latency would be
+// waited for at once.
+__device__ __forceinline__ void fetch_gates4(uint32_t (&raw)[4], const __nv_bfloat16 *__restrict__ g, int row0,
+                                             int nv, int H, int h) {
+    const int lane = threadIdx.x & 31;
+    const unsigned short *src = reinterpret_cast<const unsigned short *>(g) + (size_t)(row0 + 4 * lane) * H + h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) raw[e] = g != nullptr && 4 * lane + e < nv ? src[(size_t)e * H] : 0u;
+}
+__device__ __forceinline__ void widen_gates4(float (&x)[4], uint32_t (&raw)[4]) {
+    asm volatile("" : "+r"(raw[0]), "+r"(raw[1]), "+r"(raw[2]), "+r"(raw[3]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = clamp_gate(__uint_as_float(raw[e] << 16));
 }
 
 // Sums from the block's start up to and including each of the lane's four tokens; returns
@@ -123,26 +147,148 @@ __device__ __forceinline__ float suffix_gates4(const float (&x)[4], float (&sum)
     return __shfl_sync(0xffffffffu, run, 0);
 }
 
-// One 16-byte chunk of eight bf16 values scaled by w, as three bf16 parts.  `keep` false
-// gives zeros whatever the chunk holds.
-__device__ __forceinline__ void split3(const uint4 &raw, float w, bool keep, uint4 &p0, uint4 &p1, uint4 &p2) {
+// Products and differences of fp32 pairs.
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f32x2(uint64_t x) {  // two fp32 values as a bf16 pair
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+    return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+// The two values of a bf16 pair as fp32.
+__device__ __forceinline__ uint64_t widen_bf16x2(uint32_t x) { return pair_f32(x << 16, x & 0xffff0000u); }
+
+// One 16-byte chunk of eight bf16 values scaled by w, as PARTS bf16 numbers each, every one
+// the rounding of what the earlier ones leave.  `keep` false gives zeros whatever the chunk holds.
+template <int PARTS>
+__device__ __forceinline__ void split_chunk(const uint4 &raw, float w, bool keep, uint4 (&part)[PARTS]) {
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t out[3][4];
+    const uint64_t ww = pair_f32(__float_as_uint(w), __float_as_uint(w));
+    uint32_t out[PARTS][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float lo = keep ? w * __uint_as_float(in[e] << 16) : 0.f;
-        float hi = keep ? w * __uint_as_float(in[e] & 0xffff0000u) : 0.f;
+        uint64_t x = mul_f32x2(ww, widen_bf16x2(keep ? in[e] : 0u));
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-            const uint32_t pk = pack_bf16x2(lo, hi);
-            out[part][e] = pk;
-            lo -= __uint_as_float(pk << 16);
-            hi -= __uint_as_float(pk & 0xffff0000u);
+        for (int y = 0; y < PARTS; ++y) {
+            out[y][e] = pack_f32x2(x);
+            if (y + 1 < PARTS) x = sub_f32x2(x, widen_bf16x2(out[y][e]));
         }
     }
-    p0 = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);
-    p1 = make_uint4(out[1][0], out[1][1], out[1][2], out[1][3]);
-    p2 = make_uint4(out[2][0], out[2][1], out[2][2], out[2][3]);
+#pragma unroll
+    for (int y = 0; y < PARTS; ++y) part[y] = make_uint4(out[y][0], out[y][1], out[y][2], out[y][3]);
+}
+
+// Eight lanes that hold eight 16-byte chunks of a row each exchange them, so that chunk k of
+// lane l becomes chunk l % 8 of lane (l - l % 8) + k's row: a warp's 16-byte stores then cover
+// four rows of 128 bytes instead of touching 32 rows (32 passes of the memory pipe) each.
+__device__ __forceinline__ void transpose_chunks(uint4 (&c)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j & s) continue;
+            uint4 a = c[j], b = c[j ^ s];
+            uint4 send = up ? a : b;
+            send.x = __shfl_xor_sync(0xffffffffu, send.x, s);
+            send.y = __shfl_xor_sync(0xffffffffu, send.y, s);
+            send.z = __shfl_xor_sync(0xffffffffu, send.z, s);
+            send.w = __shfl_xor_sync(0xffffffffu, send.w, s);
+            c[j] = up ? send : a;
+            c[j ^ s] = up ? b : send;
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 pack_chunk(const float *x) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+
+// What the kernels keep of a block's log-decays, in shared memory, times log2(e): for token i
+// the sum over the tokens behind it, s_i = g_{i+1} + .. + g_{C-1}, and the sum over the block.
+// Then e^{G_C - G_j} = 2^{s_j}, e^{G_i - G_j} = 2^{s_j - s_i}, e^{G_i} = 2^{sum - s_i}.  The
+// reverse scan (PREFIX) keeps the sums up to and including token i instead.  Either is summed
+// from the end at which the state's weights are near 1, so that those come from short sums
+// and the fp32 state loses nothing to a difference of two long ones.
+// Written by one warp, lane l the tokens 4 l .. 4 l + 3: a gate is one 2-byte word per row of
+// H, and read by every warp on its own it cost 32 passes of the memory pipe per load.
+template <bool PREFIX = false>
+__device__ __forceinline__ void store_gate_sums(float *s, float *sum, const float (&x)[4]) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const int lane = threadIdx.x & 31;
+    float y[4];
+    const float all = PREFIX ? prefix_gates4(x, y) : suffix_gates4(x, y);
+    *reinterpret_cast<float4 *>(&s[4 * lane]) = make_float4(y[0] * kLog2e, y[1] * kLog2e, y[2] * kLog2e, y[3] * kLog2e);
+    if (lane == 0) *sum = all * kLog2e;
+}
+
+// 2^x of both values of a pair.
+__device__ __forceinline__ uint64_t ex2_f32x2(uint64_t x) {
+    uint64_t r;
+    asm("{\n\t.reg .f32 a, b;\n\t"
+        "mov.b64 {a, b}, %1;\n\t"
+        "ex2.approx.ftz.f32 a, a;\n\t"
+        "ex2.approx.ftz.f32 b, b;\n\t"
+        "mov.b64 %0, {a, b};\n\t}"
+        : "=l"(r)
+        : "l"(x));
+    return r;
+}
+
+// MMA issue by a whole converged warp, of which `leader` (elected once) is true in one lane:
+// the descriptors stay warp-uniform values, which one lane's branch would have to move over
+// one by one in front of every instruction.
+__device__ __forceinline__ uint32_t elect_leader() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void warp_mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t leader, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -192,6 +338,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             mbar_init(&m->empty[i], 1);
             mbar_init(&m->acc_full[i], 1);
             mbar_init(&m->acc_free[i], C::GROUP);
+            mbar_init(&m->gates_ready[i], 32);
+            mbar_init(&m->gates_free[i], C::GROUP / 32 + C::SCALERS);
         }
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
@@ -212,35 +360,44 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
         record_fault(DEV_TIMEOUT);
     };
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tlimit)) != 0;
+        return warp_wait(bar, parity, abort_flag, tlimit);
     };
     // Every ring has two slots: use t of a slot is its phase t / 2, and a slot is refilled
     // only after its release of use t - 2, so that each wait below sees the phase it means.
     auto stage = [&](int t) { return sbase + (uint32_t)((t & 1) * C::STAGE); };
 
     if (warp == 0) {
-        // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int issued = 0;
-            for (int t = 0; t < nb; ++t) {
-                if (!mbar_wait(&m->empty[t & 1], (uint32_t)(((t >> 1) & 1) ^ 1), abort_flag, tlimit)) {
-                    fail();
-                    break;
-                }
+        // ---------------------------------------------------------------- TMA loads, gate sums
+        int issued = 0;
+        uint32_t raw[4];
+        float gate[4];
+        if (nb > 0) fetch_gates4(raw, p.g, start + block_of(0) * C::C, rows_of(block_of(0)), p.H, h);
+        for (int t = 0; t < nb; ++t) {
+            if (!wwait(&m->gates_free[t & 1], (uint32_t)(((t >> 1) & 1) ^ 1))) break;
+            widen_gates4(gate, raw);
+            store_gate_sums<REV>(reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (t & 1), &m->sum[t & 1], gate);
+            mbar_arrive(&m->gates_ready[t & 1]);
+            if (t + 1 < nb)
+                fetch_gates4(raw, p.g, start + block_of(t + 1) * C::C, rows_of(block_of(t + 1)), p.H, h);
+            if (!wwait(&m->empty[t & 1], (uint32_t)(((t >> 1) & 1) ^ 1))) break;
+            if (lane == 0) {
                 mbar_arrive_expect_tx(&m->full[t & 1], (uint32_t)C::LOADED);
                 const int row = start + block_of(t) * C::C, col = h * D;
 #pragma unroll
                 for (int d = 0; d < C::DB; ++d)
                     tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t & 1]);
                 tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t & 1]);
-                ++issued;
             }
-            for (int t = max(0, issued - 2); t < issued; ++t)
-                mbar_wait(&m->full[t & 1], (uint32_t)((t >> 1) & 1), nullptr, tlimit);
+            ++issued;
         }
+        if (issued < nb) fail();
+        // loads that are still in flight land before the CTA ends
+        for (int t = max(0, issued - 2); t < issued; ++t)
+            mbar_wait(&m->full[t & 1], (uint32_t)((t >> 1) & 1), nullptr, tlimit);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
+        const uint32_t leader = elect_leader();
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
             if (!wwait(&m->full[t & 1], (uint32_t)((t >> 1) & 1)) ||
@@ -250,23 +407,19 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            if (lane == 0) {  // [dims][3 x 64 columns] = A^T [part 0 | part 1 | part 2]
-                const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
-                const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
+            // [dims][3 x 64 columns] = A^T [part 0 | part 1 | part 2]
+            const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
+            const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
 #pragma unroll
-                for (int ks = 0; ks < C::C / 16; ++ks)
-                    mma_bf16_ss(tmem + C::ACC * (t & 1), desc_add(ad, ks * 2048), desc_add(bd, ks * 2048),
-                                C::ID, ks > 0 ? 1u : 0u);
-                mma_commit(&m->empty[t & 1]);
-                mma_commit(&m->acc_full[t & 1]);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < C::C / 16; ++ks)
+                warp_mma_ss(leader, tmem + C::ACC * (t & 1), desc_add(ad, ks * 2048), desc_add(bd, ks * 2048), C::ID,
+                            ks > 0 ? 1u : 0u);
+            warp_commit(leader, &m->empty[t & 1]);
+            warp_commit(leader, &m->acc_full[t & 1]);
         }
         if (!ok) fail();
-        if (lane == 0) {  // every issued MMA has finished before TMEM is freed
-            mma_commit(&m->done);
-            mbar_wait(&m->done, 0u, nullptr, tlimit);
-        }
+        warp_commit(leader, &m->done);  // every issued MMA has finished before TMEM is freed
+        mbar_wait(&m->done, 0u, nullptr, tlimit);
         __syncwarp();
     } else if (warp < 6) {
         // ---------------------------------------------------------------- epilogue: the state
@@ -293,16 +446,20 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             }
         }
         const size_t first = (size_t)p.tab.first_block(rank);
-        float gate[4], sums[4], total = 0.f;
-        if (nb > 0) load_gates4(gate, p.g, start + block_of(0) * C::C, rows_of(block_of(0)), p.H, h);
+        float total = 0.f;
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
             const int blk = block_of(t);
             const size_t at = (first + blk) * p.H + h;
-            const float G = prefix_gates4(gate, sums), decay = expf(G);
+            // gates_ready of t + 2 needs this warp's gates_free of t
+            if (!wwait(&m->gates_ready[t & 1], (uint32_t)((t >> 1) & 1))) {
+                ok = false;
+                break;
+            }
+            const float G = m->sum[t & 1], decay = exp2f(G);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
             total += G;
-            if (t + 1 < nb)
-                load_gates4(gate, p.g, start + block_of(t + 1) * C::C, rows_of(block_of(t + 1)), p.H, h);
             if (REV && p.through != nullptr) {
                 // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
                 float f = 0.f;
@@ -323,13 +480,16 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
                 if (lane == 0) p.through[at * (4 * C::NVS) + 4 * vs + q] = decay * f;
             }
-            if (p.snap != nullptr && i_ok) {
-                uint4 *d = reinterpret_cast<uint4 *>(p.snap + (at * D + i) * D + 64 * vs);
+            if (p.snap != nullptr) {
+                uint4 c[8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    d[x] = make_uint4(pack_bf16x2(X[8 * x], X[8 * x + 1]), pack_bf16x2(X[8 * x + 2], X[8 * x + 3]),
-                                      pack_bf16x2(X[8 * x + 4], X[8 * x + 5]),
-                                      pack_bf16x2(X[8 * x + 6], X[8 * x + 7]));
+                for (int x = 0; x < 8; ++x) c[x] = pack_chunk(&X[8 * x]);
+                transpose_chunks(c);
+                if (i_ok) {
+                    uint4 *d = reinterpret_cast<uint4 *>(p.snap + (at * D + (i & ~7)) * D + 64 * vs) + (lane & 7);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) d[x * (D / 8)] = c[x];
+                }
             }
             if (!wwait(&m->acc_full[t & 1], (uint32_t)((t >> 1) & 1))) {
                 ok = false;
@@ -371,28 +531,17 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < 16; ++x) d4[x] = make_float4(X[4 * x], X[4 * x + 1], X[4 * x + 2], X[4 * x + 3]);
         }
-        if (ok && p.seg_out != nullptr && vs == 0 && q == 0 && lane == 0) p.seg_total[(size_t)sg * p.H + h] = total;
+        if (ok && p.seg_out != nullptr && vs == 0 && q == 0 && lane == 0) p.seg_total[(size_t)sg * p.H + h] = total * 0.6931471805599453f;
         if (!ok) fail();
     } else {
         // ---------------------------------------------------------------- scaling warps
         const int w8 = warp - 6;
-        float *sw = reinterpret_cast<float *>(smem + C::OFF_W) + w8 * C::C;  // this warp's own copy
-        float gate[4], sums[4];
-        if (nb > 0) load_gates4(gate, p.g, start + block_of(0) * C::C, rows_of(block_of(0)), p.H, h);
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
             const int nv = rows_of(block_of(t));
-            if (REV)
-                prefix_gates4(gate, sums);
-            else
-                suffix_gates4(gate, sums);
-            if (t + 1 < nb)
-                load_gates4(gate, p.g, start + block_of(t + 1) * C::C, rows_of(block_of(t + 1)), p.H, h);
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sw[4 * lane + e] = expf(sums[e]);
-            __syncwarp();
-            if (!wwait(&m->full[t & 1], (uint32_t)((t >> 1) & 1))) {
+            const float *sg2 = reinterpret_cast<const float *>(smem + C::OFF_G) + C::C * (t & 1);
+            if (!wwait(&m->gates_ready[t & 1], (uint32_t)((t >> 1) & 1)) ||
+                !wwait(&m->full[t & 1], (uint32_t)((t >> 1) & 1))) {
                 ok = false;
                 break;
             }
@@ -402,11 +551,10 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
 #pragma unroll 2
             for (int c = w8 * 32 + lane; c < C::C * 8; c += 32 * C::SCALERS) {
                 const int r = c >> 3;
-                uint4 p0, p1, p2;
-                split3(ld_shared_v4(b + c * 16), sw[r], r < nv, p0, p1, p2);
-                st_shared_u4(b + c * 16, p0);
-                st_shared_u4(b + C::BOX + c * 16, p1);
-                st_shared_u4(b + 2 * C::BOX + c * 16, p2);
+                uint4 part[3];
+                split_chunk(ld_shared_v4(b + c * 16), exp2f(sg2[r]), r < nv, part);
+#pragma unroll
+                for (int y = 0; y < 3; ++y) st_shared_u4(b + y * C::BOX + c * 16, part[y]);
             }
             if (nv < C::C)  // rows of another sequence: 0 times what they hold could be a NaN
                 for (int d = 0; d < C::DB; ++d)
@@ -414,6 +562,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
                         st_shared_v4(stage(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             mbar_arrive(&m->ready[t & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
         }
         if (!ok) fail();
     }

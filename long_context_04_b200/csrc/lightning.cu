@@ -386,7 +386,7 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
     static const bool fits = [&] {
         cudaFuncAttributes at;
         return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
-               at.numRegs * 5 >= C::R_MISC + C::R_KV + C::R_P + C::R_O + C::R_V;
+               at.numRegs >= C::R_LAUNCH;
     }();
     if (!fits) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
@@ -394,7 +394,7 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
     la::GatedPrefillParams p;
     std::memset(&p, 0, sizeof p);
     if (!make_map(&p.tmap_q, q, T, H, D, C::C) || !make_map(&p.tmap_k, k, T, H, D, C::C) ||
-        !make_map(&p.tmap_v, v, T, H, D, C::C))
+        !make_map(&p.tmap_v, v, T, H, D, C::C) || !make_map(&p.tmap_o, o, T, H, D, 32))
         return LA_ERR_CUDA;
     if (pl.segmented) {
         la::GatedStateParams sp;
