@@ -9,19 +9,22 @@
 //   dg as in gated.cuh, from W = dP (.) s and the row sums of q . dq and k . dk of the first
 //   terms.
 //
-// A persistent CTA per SM (192 KB of tiles: q, k, v, do and S, dS, whose place P and dP take
-// once the products that read S and dS are done).  TMEM, 512 columns: s, t, dq, dk; dv takes
-// the place of s.  The decays of the first terms differ by row, so their products go to TMEM,
-// are scaled there, and the second products accumulate on top.  Eight products per block:
+// A persistent CTA per SM.  Shared memory (D = 128): q, k, v, do 32 KB each, S and dS 32 KB
+// each; P takes the place of v and dP that of S once the products that read those are done,
+// and the results are staged over S and dS on their way out.  TMEM, 512 columns: s, t, dq, dk;
+// dv takes the place of s.  The decays of the first terms differ by row, so their products
+// go to TMEM, are scaled there, and the second products accumulate on top.  Eight products:
 //   s, t; do S^T, v dS^T; k dS  ->  scaling, P, dP  ->  dP k, dP^T q, P^T do.
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
-// Warps: 0 TMA loads, gates and dg; 1 MMA issue; 2-5 (group A) scores -> P, dP, W; 6-9
+// Warps: 0 TMA loads, gate sums and dg; 1 MMA issue; 2-5 (group A) scores -> P, dP, W; 6-9
 // (group B) scaling of the first terms and their row sums.  Both groups store the results.
-// Every barrier completes one phase per block, and all warps meet at the block's end.
+// Every barrier completes one phase per block, and all warps meet at the block's end; the
+// next block's tiles are loaded while the results go out.
 //
-// HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head.
+// HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head
+// (2304 at D = 128); tensor: 8 products of 512 cycles per block.
 #pragma once
 
 #include "gated_state_tc.cuh"
@@ -31,6 +34,7 @@ namespace la {
 struct GatedBackwardParams {
     CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;  // [T][H*D], box 64 x 128
     CUtensorMap tmap_s, tmap_ds;                  // [blocks * H * D][D], box 64 x D
+    CUtensorMap tmap_dq, tmap_dk, tmap_dv;        // results, box 64 x 32
     const __nv_bfloat16 *g;
     const float *through;  // [blocks][H][4 D / 64] parts of e^{G_C} <dS, S>, or nullptr
     __nv_bfloat16 *dq, *dk, *dv, *dg;
@@ -48,12 +52,15 @@ struct GatedBackwardCfg {
     static constexpr int SBOX = D * 128;        // 64 columns x D rows of a state
     static constexpr int TILE = DB * BOX;
     static constexpr int PT = 2 * BOX;          // P or dP
-    static constexpr int OFF_Q = 0, OFF_K = TILE, OFF_V = 2 * TILE, OFF_DO = 3 * TILE;
-    static constexpr int OFF_P = 4 * TILE, OFF_DP = OFF_P + PT;   // P over S, dP over dS
-    static constexpr int OFF_F = OFF_DP + PT;   // 10 arrays of 128 floats
-    static constexpr int OFF_MISC = OFF_F + 10 * 512;
+    static constexpr int OFF_Q = 0, OFF_K = TILE, OFF_DO = 2 * TILE, OFF_V = 3 * TILE;
+    static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
+    static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
+    static constexpr int OFF_DP = OFF_S;
+    static constexpr int OFF_STAGE = OFF_S;     // 8 KB (two boxes of 32 rows) per storing warp
+    static constexpr int OFF_F = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 8 arrays of 128 floats
+    static constexpr int OFF_MISC = OFF_F + 8 * 512;
     static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
-    static_assert(DB * SBOX <= PT, "a state fits into the place of P");
+    static_assert(DB * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
     static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     static constexpr int TM_S = 0, TM_T = 128, TM_DQ = 256, TM_DK = 384, TM_DV = 0;
     static constexpr int THREADS = 64 + 256;
@@ -65,11 +72,13 @@ struct GatedBackwardCfg {
 
 struct GatedBackwardMisc {
     uint64_t full_qk, full_vo, full_ss;   // tiles landed
-    uint64_t gates;                       // decays of the block written
-    uint64_t s_full, first_full, dv_full; // s and t; do S^T and v dS^T; k dS
+    uint64_t gates;                       // gate sums of the block written
+    uint64_t first_full, dv_full;         // s, t, do S^T and v dS^T; k dS
     uint64_t s_free;                      // group A has read s
     uint64_t p_ready, scaled, out_full;
+    uint64_t stage_free;                  // the results have left their staging place
     uint64_t done;
+    float sum;                            // log-decay of the block, times log2(e)
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -98,10 +107,8 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                                                 ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     GatedBackwardMisc *m = reinterpret_cast<GatedBackwardMisc *>(smem + C::OFF_MISC);
-    float *sG2 = reinterpret_cast<float *>(smem + C::OFF_F);  // G_i log2(e)
-    float *sGam = sG2 + 128;   // e^{G_i}
-    float *sWt = sGam + 128;   // e^{G_C - G_j}
-    float *sR = sWt + 128;     // q_i . (first term of dq_i)
+    float *sG = reinterpret_cast<float *>(smem + C::OFF_F);  // gate sums (store_gate_sums)
+    float *sR = sG + 128;      // q_i . (first term of dq_i)
     float *sE = sR + 128;      // k_j . (first term of dk_j)
     float *sRow = sE + 128;    // sum_{j < i} W_ij
     float *sCol = sRow + 128;  // [4][128]: each warp's part of sum_{i > j} W_ij
@@ -115,13 +122,13 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         mbar_init(&m->full_vo, 1);
         mbar_init(&m->full_ss, 1);
         mbar_init(&m->gates, 32);
-        mbar_init(&m->s_full, 1);
         mbar_init(&m->first_full, 1);
         mbar_init(&m->dv_full, 1);
         mbar_init(&m->s_free, 128);
         mbar_init(&m->p_ready, 128);
         mbar_init(&m->scaled, 128);
         mbar_init(&m->out_full, 1);
+        mbar_init(&m->stage_free, 8);
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
         fence_mbarrier_init_cluster();
@@ -145,31 +152,51 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
-    uint32_t load_phase = 1;      // of thread 0: the phase of its last loads
-    auto load = [&](int x) {      // thread 0: the tiles of tile x
-        load_phase ^= 1u;
+    // Loads of tile x, by a whole warp; the states' part apart, into the results' staging place.
+    int loads = 0, state_loads = 0;
+    auto load_tiles = [&](int x) {
         int rank, blk, start, len, sid;
         p.tab.block(x / p.H, rank, blk);
         p.tab.seqs.get(rank, start, len, sid);
         const int row = start + blk * C::C, col = (x % p.H) * D;
+        ++loads;
+        if (lane != 0) return;
         mbar_arrive_expect_tx(&m->full_qk, 2 * C::TILE);
+#pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
             tma_load_2d(sbase + C::OFF_Q + d * C::BOX, &p.tmap_q, col + 64 * d, row, &m->full_qk);
             tma_load_2d(sbase + C::OFF_K + d * C::BOX, &p.tmap_k, col + 64 * d, row, &m->full_qk);
         }
         mbar_arrive_expect_tx(&m->full_vo, 2 * C::TILE);
+#pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
             tma_load_2d(sbase + C::OFF_DO + d * C::BOX, &p.tmap_do, col + 64 * d, row, &m->full_vo);
             tma_load_2d(sbase + C::OFF_V + d * C::BOX, &p.tmap_v, col + 64 * d, row, &m->full_vo);
         }
+    };
+    auto load_states = [&](int x) {
+        ++state_loads;
+        if (lane != 0) return;
         mbar_arrive_expect_tx(&m->full_ss, (p.have_s + p.have_ds) * C::DB * C::SBOX);
+#pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
-            if (p.have_s) tma_load_2d(sbase + C::OFF_P + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_ss);
-            if (p.have_ds) tma_load_2d(sbase + C::OFF_DP + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ss);
+            if (p.have_s) tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_ss);
+            if (p.have_ds) tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ss);
         }
     };
-
-    if (tid == 0 && (int)blockIdx.x < tiles) load(blockIdx.x);
+    uint32_t raw[4];  // gates of the next tile, fetched ahead (warp 0)
+    auto fetch = [&](int x) {
+        int rank, blk, start, len, sid;
+        p.tab.block(x / p.H, rank, blk);
+        p.tab.seqs.get(rank, start, len, sid);
+        fetch_gates4(raw, p.g, start + blk * C::C, min(C::C, len - blk * C::C), p.H, x % p.H);
+    };
+    if (warp == 0 && (int)blockIdx.x < tiles) {
+        load_tiles(blockIdx.x);
+        load_states(blockIdx.x);
+        fetch(blockIdx.x);
+    }
+    const uint32_t leader = elect_leader();
     bool ok = true;
     uint32_t ph = 0;
     for (int x = blockIdx.x; x < tiles; x += gridDim.x, ph ^= 1u) {
@@ -178,6 +205,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         p.tab.block(x / p.H, rank, blk);
         p.tab.seqs.get(rank, start, len, sid);
         const int row0 = start + blk * C::C, nv = min(C::C, len - blk * C::C);
+        const int next = x + (int)gridDim.x;
         if (nv < C::C) {
             // rows of the next sequence must not enter any sum over the block's tokens
             if (ok) ok = wwait(&m->full_qk, ph) && wwait(&m->full_vo, ph);
@@ -189,24 +217,15 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         }
         if (warp == 0) {
             // ------------------------------------------------------------ gates, loads, dg
-            uint32_t raw[4];
-            float gate[4], sums[4], aft[4];
-            fetch_gates4(raw, p.g, row0, nv, p.H, h);
+            float gate[4];
             widen_gates4(gate, raw);
-            prefix_gates4(gate, sums);
-            suffix_gates4(gate, aft);
+            store_gate_sums(sG, &m->sum, gate);
+            mbar_arrive(&m->gates);
+            if (next < tiles) fetch(next);
             float part = 0.f;
             if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sG2[4 * lane + e] = sums[e] * 1.4426950408889634f;
-                sGam[4 * lane + e] = expf(sums[e]);
-                sWt[4 * lane + e] = expf(aft[e]);
-            }
-            mbar_arrive(&m->gates);
             if (ok) ok = wwait(&m->out_full, ph);
-            // every product that reads the tiles is done
-            if (ok && lane == 0 && x + (int)gridDim.x < tiles) load(x + gridDim.x);
+            if (ok && next < tiles) load_tiles(next);  // every product that reads the tiles is done
             // group A's and group B's sums were written before the products of out_full were
             // issued, but this warp has to see them itself
             if (ok) ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
@@ -231,6 +250,8 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             __float2bfloat16_rn(part + (up[y] + r[y]) + (down[y] - e[y]));
                 }
             }
+            if (ok) ok = wwait(&m->stage_free, ph);
+            if (ok && next < tiles) load_states(next);
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
@@ -242,74 +263,51 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             // D (+)= A B over n steps of 16; `keep` adds to what D holds
             auto product = [&](uint32_t d, uint64_t a, auto at_a, uint64_t b, auto at_b, uint32_t id, int n,
                                bool keep) {
-                mma_bf16_ss(tmem + d, desc_add(a, at_a(0)), desc_add(b, at_b(0)), id, keep ? 1u : 0u);
-#pragma unroll
-                for (int ks = 1; ks < n; ++ks)
-                    mma_bf16_ss(tmem + d, desc_add(a, at_a(ks)), desc_add(b, at_b(ks)), id, 1u);
+#pragma unroll 2
+                for (int ks = 0; ks < n; ++ks)
+                    warp_mma_ss(leader, tmem + d, desc_add(a, at_a(ks)), desc_add(b, at_b(ks)), id,
+                                keep || ks > 0 ? 1u : 0u);
             };
             const uint64_t qk = desc_kmajor_sw128(sbase + C::OFF_Q), kkd = desc_kmajor_sw128(sbase + C::OFF_K),
                            vk = desc_kmajor_sw128(sbase + C::OFF_V), ok_ = desc_kmajor_sw128(sbase + C::OFF_DO);
             if (ok) ok = wwait(&m->full_qk, ph);
             if (ok) {
                 tc_fence_after();
-                if (lane == 0) product(C::TM_S, qk, kk, kkd, kk, C::ID_S, D / 16, false);
-                __syncwarp();
+                product(C::TM_S, qk, kk, kkd, kk, C::ID_S, D / 16, false);
                 ok = wwait(&m->full_vo, ph);
             }
             if (ok) {
                 tc_fence_after();
-                if (lane == 0) {
-                    product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
-                    mma_commit(&m->s_full);
-                }
-                __syncwarp();
+                product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
                 ok = wwait(&m->full_ss, ph);
             }
             if (ok) {
                 tc_fence_after();
-                // (Uniform branches around the elected thread's, not inside it: nested the other
-                // way, the first product instruction behind the inner test went missing at D = 64.)
-                if (p.have_s) {
-                    if (lane == 0)
-                        product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_P), ss, C::ID_KK, D / 16, false);
-                    __syncwarp();
-                }
-                if (p.have_ds) {
-                    if (lane == 0)
-                        product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DP), ss, C::ID_KK, D / 16, false);
-                    __syncwarp();
-                }
-                if (lane == 0) mma_commit(&m->first_full);
-                __syncwarp();
+                if (p.have_s)
+                    product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
+                if (p.have_ds)
+                    product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
+                warp_commit(leader, &m->first_full);
                 ok = wwait(&m->s_free, ph);
             }
             if (ok) {
                 tc_fence_after();
-                if (p.have_ds) {
-                    if (lane == 0)
-                        product(C::TM_DV, kkd, kk, desc_mnmajor_sw128(sbase + C::OFF_DP, C::SBOX), nn, C::ID_KN,
-                                D / 16, false);
-                    __syncwarp();
-                }
-                if (lane == 0) mma_commit(&m->dv_full);
-                __syncwarp();
+                if (p.have_ds)
+                    product(C::TM_DV, kkd, kk, desc_mnmajor_sw128(sbase + C::OFF_DS, C::SBOX), nn, C::ID_KN, D / 16,
+                            false);
+                warp_commit(leader, &m->dv_full);
                 ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
             }
             if (ok) {
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t dpk = desc_kmajor_sw128(sbase + C::OFF_DP),
-                                   dpn = desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX),
-                                   pn = desc_mnmajor_sw128(sbase + C::OFF_P, C::BOX),
-                                   qn = desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX),
-                                   kn = desc_mnmajor_sw128(sbase + C::OFF_K, C::BOX),
-                                   on = desc_mnmajor_sw128(sbase + C::OFF_DO, C::BOX);
-                    product(C::TM_DQ, dpk, kk, kn, nn, C::ID_KN, C::C / 16, p.have_s != 0);
-                    product(C::TM_DK, dpn, nn, qn, nn, C::ID_NN, C::C / 16, p.have_ds != 0);
-                    product(C::TM_DV, pn, nn, on, nn, C::ID_NN, C::C / 16, p.have_ds != 0);
-                    mma_commit(&m->out_full);
-                }
-                __syncwarp();
+                const uint64_t dpn = desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX);
+                product(C::TM_DQ, desc_kmajor_sw128(sbase + C::OFF_DP), kk, desc_mnmajor_sw128(sbase + C::OFF_K, C::BOX),
+                        nn, C::ID_KN, C::C / 16, p.have_s != 0);
+                product(C::TM_DK, dpn, nn, desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16,
+                        p.have_ds != 0);
+                product(C::TM_DV, desc_mnmajor_sw128(sbase + C::OFF_P, C::BOX), nn,
+                        desc_mnmajor_sw128(sbase + C::OFF_DO, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
+                warp_commit(leader, &m->out_full);
             }
         } else {
             const int q = warp & 3;
@@ -317,59 +315,73 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             const uint32_t lanes = (uint32_t)(32 * q) << 16;
             if (warp < 6) {
                 // -------------------------------------------------------- group A: P, dP, W
-                uint32_t pp[64], dd[64];                       // packed rows of P and dP
-                if (ok) ok = wwait(&m->gates, ph) && wwait(&m->s_full, ph);
+                // (behind first_full v and S have been read: P and dP may take their places)
+                if (ok) ok = wwait(&m->gates, ph) && wwait(&m->first_full, ph);
                 if (ok) {
                     tc_fence_after();
-                    const float Gi = sG2[i];
+                    const uint32_t si = __float_as_uint(sG[i]);
+                    const uint64_t s2 = pair_f32(si, si);
                     float row = 0.f;
-#pragma unroll
+#pragma unroll 1
                     for (int cc = 0; cc < 4; ++cc) {
+                        uint32_t P[16], dP[16];                // packed 32 columns
+                        float col = 0.f;
                         if (cc <= q) {                         // columns that the rows of this warp see
-                            uint32_t s[32], t[32];
-                            tmem_ld32(tmem + C::TM_S + 32 * cc + lanes, s);
+                            uint32_t sc[32], t[32];
+                            tmem_ld32(tmem + C::TM_S + 32 * cc + lanes, sc);
                             tmem_ld32(tmem + C::TM_T + 32 * cc + lanes, t);
                             tmem_ld_wait();
                             float w[32];
+                            const int seen = cc < q ? 32 : lane;  // columns before this row
 #pragma unroll
                             for (int y = 0; y < 32; y += 4) {
-                                const float4 Gj = *reinterpret_cast<const float4 *>(&sG2[32 * cc + y]);
-                                const float gj[4] = {Gj.x, Gj.y, Gj.z, Gj.w};
-                                float P[4], dP[4];
+                                const ulonglong2 sj = *reinterpret_cast<const ulonglong2 *>(&sG[32 * cc + y]);
 #pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const bool seen = cc < q || y + z <= lane;
-                                    const float d = ex2(Gi - gj[z]);
-                                    P[z] = seen ? __uint_as_float(s[y + z]) * d : 0.f;
-                                    dP[z] = seen ? __uint_as_float(t[y + z]) * d : 0.f;
-                                    w[y + z] = cc < q || y + z < lane ? P[z] * __uint_as_float(t[y + z]) : 0.f;
-                                    row += w[y + z];
+                                for (int z = 0; z < 4; z += 2) {
+                                    const uint64_t d = ex2_f32x2(sub_f32x2(z == 0 ? sj.x : sj.y, s2));
+                                    const uint64_t tt = pair_f32(t[y + z], t[y + z + 1]);
+                                    const uint64_t pp = mul_f32x2(pair_f32(sc[y + z], sc[y + z + 1]), d);
+                                    P[(y + z) / 2] = pack_f32x2(pp);
+                                    dP[(y + z) / 2] = pack_f32x2(mul_f32x2(tt, d));
+                                    uint32_t lo, hi;
+                                    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(mul_f32x2(pp, tt)));
+                                    w[y + z] = y + z < seen ? __uint_as_float(lo) : 0.f;
+                                    w[y + z + 1] = y + z + 1 < seen ? __uint_as_float(hi) : 0.f;
                                 }
-                                pp[16 * cc + y / 2] = pack_bf16x2(P[0], P[1]);
-                                pp[16 * cc + y / 2 + 1] = pack_bf16x2(P[2], P[3]);
-                                dd[16 * cc + y / 2] = pack_bf16x2(dP[0], dP[1]);
-                                dd[16 * cc + y / 2 + 1] = pack_bf16x2(dP[2], dP[3]);
                             }
-                            sCol[128 * q + 32 * cc + lane] = warp_column_sums(w);
+                            if (cc == q) {  // columns behind this row, whatever they hold, give 0
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) {
+                                    const uint32_t mask = 2 * y + 1 <= lane ? 0xffffffffu
+                                                          : 2 * y <= lane   ? 0x0000ffffu
+                                                                            : 0u;
+                                    P[y] &= mask;
+                                    dP[y] &= mask;
+                                }
+                            }
+                            float r0 = 0.f, r1 = 0.f;
+#pragma unroll
+                            for (int y = 0; y < 32; y += 2) r0 += w[y], r1 += w[y + 1];
+                            row += r0 + r1;
+                            col = warp_column_sums(w);
                         } else {
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) pp[16 * cc + y] = dd[16 * cc + y] = 0u;
-                            sCol[128 * q + 32 * cc + lane] = 0.f;
+                            for (int y = 0; y < 16; ++y) P[y] = dP[y] = 0u;
+                        }
+                        sCol[128 * q + 32 * cc + lane] = col;
+                        const uint32_t at = sbase + (uint32_t)((cc >> 1) * C::BOX + i * 128);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t o = at + (((4 * (cc & 1) + c) ^ (i & 7)) << 4);
+                            st_shared_v4(C::OFF_P + o, P[4 * c], P[4 * c + 1], P[4 * c + 2], P[4 * c + 3]);
+                            st_shared_v4(C::OFF_DP + o, dP[4 * c], dP[4 * c + 1], dP[4 * c + 2], dP[4 * c + 3]);
+                        }
+                        if (cc == q) {                         // the last columns of s and t that are read
+                            tc_fence_before();
+                            mbar_arrive(&m->s_free);
                         }
                     }
                     sRow[i] = row;
-                    tc_fence_before();
-                    mbar_arrive(&m->s_free);
-                    // the products that read S and dS are done: their place is free
-                    ok = wwait(&m->first_full, ph) && wwait(&m->dv_full, ph);
-                }
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint32_t at = (uint32_t)((c >> 3) * C::BOX + i * 128 + (((c & 7) ^ (i & 7)) << 4));
-                        st_shared_v4(sbase + C::OFF_P + at, pp[4 * c], pp[4 * c + 1], pp[4 * c + 2], pp[4 * c + 3]);
-                        st_shared_v4(sbase + C::OFF_DP + at, dd[4 * c], dd[4 * c + 1], dd[4 * c + 2], dd[4 * c + 3]);
-                    }
                     fence_proxy_async_smem();
                     mbar_arrive(&m->p_ready);
                 }
@@ -407,14 +419,15 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                         }
                     };
                     float none = 0.f;
-                    if (p.have_s) scale(C::TM_DQ, sGam[i], C::OFF_Q, r);
-                    if (p.have_ds) scale(C::TM_DK, sWt[i], C::OFF_K, e);
+                    const float wt = ex2(sG[i]), gam = ex2(m->sum - sG[i]);  // e^{G_C - G_i}, e^{G_i}
+                    if (p.have_s) scale(C::TM_DQ, gam, C::OFF_Q, r);
+                    if (p.have_ds) scale(C::TM_DK, wt, C::OFF_K, e);
                     sR[i] = r;
                     sE[i] = e;
                     ok = wwait(&m->dv_full, ph);
                     if (ok) {
                         tc_fence_after();
-                        if (p.have_ds) scale(C::TM_DV, sWt[i], -1, none);
+                        if (p.have_ds) scale(C::TM_DV, wt, -1, none);
                         tmem_st_wait();
                         tc_fence_before();
                         mbar_arrive(&m->scaled);
@@ -425,31 +438,56 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             if (ok) ok = wwait(&m->out_full, ph);
             if (ok) {
                 tc_fence_after();
-                auto store = [&](uint32_t col, __nv_bfloat16 *out, int c0, int c1) {
+                // A box of 64 columns goes through this warp's staging place `slot` to global memory.
+                // (Stores from registers would touch 32 rows each: 32 passes of the memory pipe.)
+                const uint32_t stage = sbase + C::OFF_STAGE + (warp - 2) * 8192;
+                auto store = [&](int slot, uint32_t col, const CUtensorMap *map, __nv_bfloat16 *out, int box) {
+                    const uint32_t to = stage + slot * 4096;
 #pragma unroll 1
-                    for (int cc = c0; cc < c1; ++cc) {
+                    for (int cc = 0; cc < 2; ++cc) {
                         uint32_t a[32];
-                        tmem_ld32(tmem + col + 32 * cc + lanes, a);
+                        tmem_ld32(tmem + col + 64 * box + 32 * cc + lanes, a);
                         tmem_ld_wait();
-                        if (i < nv) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(row0 + i) * p.H + h) * D + 32 * cc);
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                dst[y] = make_uint4(
-                                    pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
-                                    pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
-                                    pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
-                                    pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                        for (int y = 0; y < 4; ++y)
+                            st_shared_v4(to + lane * 128 + (((4 * cc + y) ^ (lane & 7)) << 4),
+                                         pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
+                                         pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
+                                         pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
+                                         pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                    }
+                    if (32 * q + 32 <= nv) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(map, to, h * D + 64 * box, row0 + 32 * q);
+                            bulk_commit_group();
                         }
+                    } else if (i < nv) {  // the sequence's last rows, one lane each
+                        uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(row0 + i) * p.H + h) * D + 64 * box);
+#pragma unroll 1
+                        for (int z = 0; z < 8; ++z) dst[z] = ld_shared_v4(to + lane * 128 + ((z ^ (lane & 7)) << 4));
                     }
                 };
-                if (warp < 6) {
-                    store(C::TM_DK, p.dk, 0, D / 32);
-                    store(C::TM_DV, p.dv, 0, D / 64);
-                } else {
-                    store(C::TM_DQ, p.dq, 0, D / 32);
-                    store(C::TM_DV, p.dv, D / 64, D / 32);
+                // group A: dk and (D = 128) dv's second half; group B: dq and dv's first half
+                const bool A = warp < 6;
+                const int boxes = D == 128 ? 3 : A ? 1 : 2;
+#pragma unroll 1
+                for (int n = 0; n < boxes; ++n) {
+                    const bool dv = n == D / 64;
+                    if (n == 2) {
+                        if (lane == 0) bulk_wait_read_all();
+                        __syncwarp();
+                    }
+                    store(n & 1, dv ? C::TM_DV : A ? C::TM_DK : C::TM_DQ,
+                          dv ? &p.tmap_dv : A ? &p.tmap_dk : &p.tmap_dq, dv ? p.dv : A ? p.dk : p.dq,
+                          dv ? (D == 128 && A ? 1 : 0) : n);
                 }
+                if (lane == 0) {
+                    bulk_wait_read_all();
+                    mbar_arrive(&m->stage_free);
+                }
+                __syncwarp();
                 tc_fence_before();
             }
         }
@@ -461,13 +499,16 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         }
         tc_fence_after();
     }
-    if (tid == 0 && !ok) {  // loads that are still in flight land before the CTA ends
-        mbar_wait(&m->full_qk, load_phase, nullptr, tlimit);
-        mbar_wait(&m->full_vo, load_phase, nullptr, tlimit);
-        mbar_wait(&m->full_ss, load_phase, nullptr, tlimit);
+    if (warp == 0 && !ok) {  // loads that are still in flight land before the CTA ends
+        if (loads > 0) {
+            mbar_wait(&m->full_qk, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
+            mbar_wait(&m->full_vo, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
+        }
+        if (state_loads > 0) mbar_wait(&m->full_ss, (uint32_t)((state_loads - 1) & 1), nullptr, tlimit);
     }
-    if (warp == 1 && lane == 0) {  // every issued MMA has finished before TMEM is freed
-        mma_commit(&m->done);
+    if (warp >= 2 && lane == 0) bulk_wait_all();
+    if (warp == 1) {  // every issued MMA has finished before TMEM is freed
+        warp_commit(leader, &m->done);
         mbar_wait(&m->done, 0u, nullptr, tlimit);
     }
     tc_fence_before();
