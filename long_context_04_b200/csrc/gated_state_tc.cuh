@@ -10,9 +10,9 @@
 // factor (128 x D) and the slice of the right one (128 x 64) arrive by TMA; six warps scale
 // the slice's rows by their decays and split every product into three bf16 numbers whose sum
 // is the fp32 product to 2^-26 (one bf16 alone would round the state by 2^-9 in every step);
-// one thread issues a single product [D x 128] [128 x 192] of the tile with the three parts
-// side by side (one read of the left factor from shared memory instead of three), and the
-// epilogue adds the three accumulators to the fp32 state in its registers.
+// one warp issues the product of the tile with the first two parts side by side (one read of
+// the left factor from shared memory for both) and adds that with the third to the second's
+// columns; the epilogue adds the two accumulators to the fp32 state in its registers.
 //
 // The tensor work (3 x 2 D^2 flops per token) is below its HBM time: 4 D bytes read (the left
 // tile is read by D / 64 CTAs, mostly from L2) and 2 D^2 / 128 bytes of snapshot written per
@@ -56,11 +56,11 @@ struct GatedStateCfg {
     // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
     static constexpr int SMEM_BYTES = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-    static constexpr int TMEM_COLS = 512;           // two accumulators of 192 columns
-    static constexpr int ACC = 256;                 // columns from one accumulator to the other
+    static constexpr int TMEM_COLS = 256;           // two accumulators of 128 columns
+    static constexpr int ACC = 128;
     static constexpr int GROUP = 128;               // epilogue threads
     static constexpr int THREADS = 64 + GROUP + 32 * SCALERS;
-    static constexpr uint32_t ID = idesc_bf16_f32(D, 192, 1, 1);
+    static constexpr uint32_t ID2 = idesc_bf16_f32(D, 128, 1, 1), ID1 = idesc_bf16_f32(D, 64, 1, 1);
 };
 
 struct GatedStateMisc {
@@ -250,6 +250,17 @@ __device__ __forceinline__ uint64_t ex2_f32x2(uint64_t x) {
     return r;
 }
 
+// 16 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // MMA issue by a whole converged warp, of which `leader` (elected once) is true in one lane:
 // the descriptors stay warp-uniform values, which one lane's branch would have to move over
 // one by one in front of every instruction.
@@ -407,13 +418,17 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            // [dims][3 x 64 columns] = A^T [part 0 | part 1 | part 2]
+            // [dims][2 x 64 columns] = A^T [part 0 | part 1 + part 2]
             const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
             const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
-#pragma unroll
+#pragma unroll 2
             for (int ks = 0; ks < C::C / 16; ++ks)
-                warp_mma_ss(leader, tmem + C::ACC * (t & 1), desc_add(ad, ks * 2048), desc_add(bd, ks * 2048), C::ID,
+                warp_mma_ss(leader, tmem + C::ACC * (t & 1), desc_add(ad, ks * 2048), desc_add(bd, ks * 2048), C::ID2,
                             ks > 0 ? 1u : 0u);
+#pragma unroll 2
+            for (int ks = 0; ks < C::C / 16; ++ks)
+                warp_mma_ss(leader, tmem + C::ACC * (t & 1) + 64, desc_add(ad, ks * 2048),
+                            desc_add(bd, 2 * C::BOX + ks * 2048), C::ID1, 1u);
             warp_commit(leader, &m->empty[t & 1]);
             warp_commit(leader, &m->acc_full[t & 1]);
         }
@@ -446,6 +461,17 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             }
         }
         const size_t first = (size_t)p.tab.first_block(rank);
+        // the forward snapshot's rows of this warp, fetched a block ahead: chunk lane % 8 of the
+        // eight rows that transpose_chunks hands on
+        uint4 o[8];
+        auto fetch_other = [&](int t) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                   p.other + (((first + block_of(t)) * p.H + h) * D + (i & ~7)) * D + 64 * vs) +
+                               (lane & 7);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = i_ok ? src[x * (D / 8)] : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (REV && p.through != nullptr && nb > 0) fetch_other(0);
         float total = 0.f;
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
@@ -462,20 +488,19 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             total += G;
             if (REV && p.through != nullptr) {
                 // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
-                float f = 0.f;
-                if (i_ok) {
-                    const uint4 *o = reinterpret_cast<const uint4 *>(p.other + (at * D + i) * D + 64 * vs);
+                transpose_chunks(o);
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 w = o[x];
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t in[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            f = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], f);
-                            f = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], f);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
+                        part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
                     }
                 }
+                float f = i_ok ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
+                if (t + 1 < nb) fetch_other(t + 1);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
                 if (lane == 0) p.through[at * (4 * C::NVS) + 4 * vs + q] = decay * f;
@@ -498,27 +523,18 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             tc_fence_after();
             const uint32_t tA = tmem + C::ACC * (t & 1) + lane_base;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t a[32];
-                // the smallest part first
-                tmem_ld32(tA + 128 + 32 * half, a);
+            for (int x = 0; x < 4; ++x) {
+                uint32_t a[16], c[16];
+                tmem_ld16(tA + 16 * x, a);
+                tmem_ld16(tA + 64 + 16 * x, c);
                 tmem_ld_wait();
-                float lo[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) lo[x] = __uint_as_float(a[x]);
-                tmem_ld32(tA + 64 + 32 * half, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int x = 0; x < 32; ++x) lo[x] += __uint_as_float(a[x]);
-                tmem_ld32(tA + 32 * half, a);
-                tmem_ld_wait();
-                if (half == 1) {
+                if (x == 3) {
                     tc_fence_before();
                     mbar_arrive(&m->acc_free[t & 1]);
                 }
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    X[32 * half + x] = fmaf(decay, X[32 * half + x], lo[x] + __uint_as_float(a[x]));
+                for (int z = 0; z < 16; ++z)
+                    X[16 * x + z] = fmaf(decay, X[16 * x + z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
             }
         }
         float *to = nullptr;
