@@ -11,15 +11,16 @@
 //
 // A persistent CTA per SM.  Shared memory (D = 128): q, k, v, do 32 KB each, S and dS 32 KB
 // each; P takes the place of v and dP that of S once the products that read those are done,
-// and the results are staged over S and dS on their way out.  TMEM, 512 columns: s, t, dq, dk;
-// dv takes the place of s.  The decays of the first terms differ by row, so their products
-// go to TMEM, are scaled there, and the second products accumulate on top.  Eight products:
-//   s, t; do S^T, v dS^T; k dS  ->  scaling, P, dP  ->  dP k, dP^T q, P^T do.
+// and results are staged over S and dS on their way out.  TMEM, 512 columns: s, t, dq, dk; the
+// two terms of dv take the places of s and t.  The decays of the first terms differ by row:
+// those of dq and dk are scaled in TMEM and the second products accumulate on top, the two of
+// dv are added on the way out.  Eight products, in this order:
+//   s, t; do S^T, v dS^T  ->  P, dP; scaling  ->  k dS; P^T do; dP^T q, dP k.
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
-// Warps: 0 TMA loads, gate sums and dg; 1 MMA issue; 2-5 (group A) scores -> P, dP, W; 6-9
-// (group B) scaling of the first terms and their row sums.  Both groups store the results.
+// Warps: 0 TMA loads and gate sums; 1 MMA issue and dg; 2-9 (group A) scores -> P, dP, W, then
+// dv and dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out.
 // Every barrier completes one phase per block, and all warps meet at the block's end; the
 // next block's tiles are loaded while the results go out.
 //
@@ -56,14 +57,16 @@ struct GatedBackwardCfg {
     static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
     static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
     static constexpr int OFF_DP = OFF_S;
-    static constexpr int OFF_STAGE = OFF_S;     // 8 KB (two boxes of 32 rows) per storing warp
-    static constexpr int OFF_F = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 8 arrays of 128 floats
-    static constexpr int OFF_MISC = OFF_F + 8 * 512;
+    // staging boxes of 64 columns x 32 rows: dv over dS and dk over dP (eight warps of group A),
+    // dq beside them (group B)
+    static constexpr int OFF_STAGE = OFF_S + 2 * PT + (D == 128 ? 0 : PT);
+    static constexpr int OFF_F = OFF_STAGE + 4 * 4096;          // 9 arrays of 128 floats
+    static constexpr int OFF_MISC = OFF_F + 9 * 512;
     static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
     static_assert(DB * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
     static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
-    static constexpr int TM_S = 0, TM_T = 128, TM_DQ = 256, TM_DK = 384, TM_DV = 0;
-    static constexpr int THREADS = 64 + 256;
+    static constexpr int TM_S = 0, TM_T = 128, TM_DQ = 256, TM_DK = 384, TM_DV1 = 0, TM_DV2 = 128;
+    static constexpr int GROUP_A = 256, GROUP_B = 128, THREADS = 64 + GROUP_A + GROUP_B;
     static constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, 0, 0);
     static constexpr uint32_t ID_KK = idesc_bf16_f32(128, D, 0, 0);
     static constexpr uint32_t ID_KN = idesc_bf16_f32(128, D, 0, 1);
@@ -73,21 +76,22 @@ struct GatedBackwardCfg {
 struct GatedBackwardMisc {
     uint64_t full_qk, full_vo, full_ss;   // tiles landed
     uint64_t gates;                       // gate sums of the block written
-    uint64_t first_full, dv_full;         // s, t, do S^T and v dS^T; k dS
-    uint64_t s_free;                      // group A has read s
-    uint64_t p_ready, scaled, out_full;
-    uint64_t stage_free;                  // the results have left their staging place
+    uint64_t first_full;                  // s, t, do S^T, v dS^T
+    uint64_t s_free;                      // group A has read s and t
+    uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
+    uint64_t dv_full, out_full;           // dv; dq and dk
+    uint64_t stage_free;                  // group A's results have left the places of S and dS
     uint64_t done;
     float sum;                            // log-decay of the block, times log2(e)
     uint32_t tmem_base;
     int abort_flag;
 };
 
-// w[x] of every lane, summed over the warp's lanes: lane l gets the sum of w[l].
-__device__ __forceinline__ float warp_column_sums(float (&w)[32]) {
+// w[x] of every lane, summed over the warp's lanes: lane l gets the sum of w[l % 16].
+__device__ __forceinline__ float warp_column_sums(float (&w)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = 8; off > 0; off >>= 1) {
         const bool up = (lane & off) != 0;
 #pragma unroll
         for (int x = 0; x < off; ++x) {
@@ -95,7 +99,7 @@ __device__ __forceinline__ float warp_column_sums(float (&w)[32]) {
             w[x] = keep + __shfl_xor_sync(0xffffffffu, send, off);
         }
     }
-    return w[0];
+    return w[0] + __shfl_xor_sync(0xffffffffu, w[0], 16);
 }
 
 template <int D>
@@ -110,8 +114,8 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     float *sG = reinterpret_cast<float *>(smem + C::OFF_F);  // gate sums (store_gate_sums)
     float *sR = sG + 128;      // q_i . (first term of dq_i)
     float *sE = sR + 128;      // k_j . (first term of dk_j)
-    float *sRow = sE + 128;    // sum_{j < i} W_ij
-    float *sCol = sRow + 128;  // [4][128]: each warp's part of sum_{i > j} W_ij
+    float *sRow = sE + 128;    // [2][128]: parts of sum_{j < i} W_ij
+    float *sCol = sRow + 256;  // [4][128]: parts of sum_{i > j} W_ij, by 32 rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const uint64_t tlimit = p.timeout_ns;
     volatile int *abort_flag = &m->abort_flag;
@@ -124,9 +128,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         mbar_init(&m->gates, 32);
         mbar_init(&m->first_full, 1);
         mbar_init(&m->dv_full, 1);
-        mbar_init(&m->s_free, 128);
-        mbar_init(&m->p_ready, 128);
-        mbar_init(&m->scaled, 128);
+        mbar_init(&m->s_free, C::GROUP_A);
+        mbar_init(&m->p_ready, C::GROUP_A);
+        mbar_init(&m->scaled, C::GROUP_B);
         mbar_init(&m->out_full, 1);
         mbar_init(&m->stage_free, 8);
         mbar_init(&m->done, 1);
@@ -216,40 +220,14 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             __syncthreads();
         }
         if (warp == 0) {
-            // ------------------------------------------------------------ gates, loads, dg
+            // ------------------------------------------------------------ gate sums, loads
             float gate[4];
             widen_gates4(gate, raw);
             store_gate_sums(sG, &m->sum, gate);
             mbar_arrive(&m->gates);
             if (next < tiles) fetch(next);
-            float part = 0.f;
-            if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
             if (ok) ok = wwait(&m->out_full, ph);
             if (ok && next < tiles) load_tiles(next);  // every product that reads the tiles is done
-            // group A's and group B's sums were written before the products of out_full were
-            // issued, but this warp has to see them itself
-            if (ok) ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
-            if (ok && p.dg != nullptr) {
-                // dg_t = e^{G_C} <dS, S> + sum_{i >= t} sR_i + sum_{j < t} (sE_j + col_j - row_j)
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-                float r[4], e[4], up[4], down[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = 4 * lane + y;
-                    r[y] = sR[t];
-                    e[y] = sE[t] + (((sCol[t] + sCol[128 + t]) + (sCol[256 + t] + sCol[384 + t])) - sRow[t]);
-                }
-                prefix_gates4(e, down);   // down[y] = sum_{j <= t}
-                suffix_gates4(r, up);     // up[y] = sum_{i > t}
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = 4 * lane + y;
-                    if (t < nv)
-                        p.dg[(size_t)(row0 + t) * p.H + h] =
-                            __float2bfloat16_rn(part + (up[y] + r[y]) + (down[y] - e[y]));
-                }
-            }
             if (ok) ok = wwait(&m->stage_free, ph);
             if (ok && next < tiles) load_states(next);
             __syncwarp();
@@ -290,52 +268,127 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 warp_commit(leader, &m->first_full);
                 ok = wwait(&m->s_free, ph);
             }
+            float part = 0.f;
+            if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
             if (ok) {
                 tc_fence_after();
                 if (p.have_ds)
-                    product(C::TM_DV, kkd, kk, desc_mnmajor_sw128(sbase + C::OFF_DS, C::SBOX), nn, C::ID_KN, D / 16,
+                    product(C::TM_DV1, kkd, kk, desc_mnmajor_sw128(sbase + C::OFF_DS, C::SBOX), nn, C::ID_KN, D / 16,
                             false);
-                warp_commit(leader, &m->dv_full);
-                ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
+                ok = wwait(&m->p_ready, ph);
             }
             if (ok) {
                 tc_fence_after();
-                const uint64_t dpn = desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX);
+                product(C::TM_DV2, desc_mnmajor_sw128(sbase + C::OFF_P, C::BOX), nn,
+                        desc_mnmajor_sw128(sbase + C::OFF_DO, C::BOX), nn, C::ID_NN, C::C / 16, false);
+                warp_commit(leader, &m->dv_full);
+                ok = wwait(&m->scaled, ph);
+            }
+            if (ok) {
+                tc_fence_after();
+                product(C::TM_DK, desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX), nn,
+                        desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
                 product(C::TM_DQ, desc_kmajor_sw128(sbase + C::OFF_DP), kk, desc_mnmajor_sw128(sbase + C::OFF_K, C::BOX),
                         nn, C::ID_KN, C::C / 16, p.have_s != 0);
-                product(C::TM_DK, dpn, nn, desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16,
-                        p.have_ds != 0);
-                product(C::TM_DV, desc_mnmajor_sw128(sbase + C::OFF_P, C::BOX), nn,
-                        desc_mnmajor_sw128(sbase + C::OFF_DO, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
                 warp_commit(leader, &m->out_full);
             }
+            if (ok && p.dg != nullptr) {
+                // dg_t = e^{G_C} <dS, S> + sum_{i >= t} sR_i + sum_{j < t} (sE_j + col_j - row_j)
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+                float r[4], e[4], up[4], down[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int t = 4 * lane + y;
+                    r[y] = sR[t];
+                    e[y] = sE[t] + (((sCol[t] + sCol[128 + t]) + (sCol[256 + t] + sCol[384 + t])) -
+                                    (sRow[t] + sRow[128 + t]));
+                }
+                prefix_gates4(e, down);   // down[y] = sum_{j <= t}
+                suffix_gates4(r, up);     // up[y] = sum_{i > t}
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int t = 4 * lane + y;
+                    if (t < nv)
+                        p.dg[(size_t)(row0 + t) * p.H + h] =
+                            __float2bfloat16_rn(part + (up[y] + r[y]) + (down[y] - e[y]));
+                }
+            }
+            __syncwarp();
         } else {
             const int q = warp & 3;
             const int i = 32 * q + lane;                       // this thread's row
             const uint32_t lanes = (uint32_t)(32 * q) << 16;
-            if (warp < 6) {
+            const bool A = warp < 2 + C::GROUP_A / 32;
+            const int half = A ? (warp - 2) >> 2 : 0;
+            // A box of 64 columns, times w where `twice` adds a second accumulator, goes through this
+            // warp's staging place to global memory.  (Stores from registers would touch 32 rows
+            // each: 32 passes of the memory pipe.)
+            auto store = [&](uint32_t stage, uint32_t col, bool twice, float w, const CUtensorMap *map,
+                             __nv_bfloat16 *out, int box) {
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t a[16];
+                    tmem_ld16(tmem + col + 64 * box + 16 * cc + lanes, a);
+                    if (twice) {
+                        uint32_t c[16];
+                        tmem_ld16(tmem + C::TM_DV1 + 64 * box + 16 * cc + lanes, c);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            a[y] = __float_as_uint(fmaf(w, __uint_as_float(c[y]), __uint_as_float(a[y])));
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        st_shared_v4(stage + lane * 128 + (((2 * cc + y) ^ (lane & 7)) << 4),
+                                     pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                }
+                if (32 * q + 32 <= nv) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(map, stage, h * D + 64 * box, row0 + 32 * q);
+                        bulk_commit_group();
+                    }
+                } else if (i < nv) {  // the sequence's last rows, one lane each
+                    uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(row0 + i) * p.H + h) * D + 64 * box);
+#pragma unroll 1
+                    for (int z = 0; z < 8; ++z) dst[z] = ld_shared_v4(stage + lane * 128 + ((z ^ (lane & 7)) << 4));
+                }
+            };
+            auto staged = [&]() {  // the warp's staging places may be written again
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            };
+            if (A) {
                 // -------------------------------------------------------- group A: P, dP, W
                 // (behind first_full v and S have been read: P and dP may take their places)
                 if (ok) ok = wwait(&m->gates, ph) && wwait(&m->first_full, ph);
+                float wt = 0.f;
                 if (ok) {
                     tc_fence_after();
                     const uint32_t si = __float_as_uint(sG[i]);
                     const uint64_t s2 = pair_f32(si, si);
+                    wt = ex2(sG[i]);
                     float row = 0.f;
 #pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        uint32_t P[16], dP[16];                // packed 32 columns
+                    for (int pc = half; pc < 8; pc += 2) {     // every other 16 columns
+                        uint32_t P[8], dP[8];                  // packed
                         float col = 0.f;
-                        if (cc <= q) {                         // columns that the rows of this warp see
-                            uint32_t sc[32], t[32];
-                            tmem_ld32(tmem + C::TM_S + 32 * cc + lanes, sc);
-                            tmem_ld32(tmem + C::TM_T + 32 * cc + lanes, t);
+                        if (pc <= 2 * q + 1) {                 // columns that rows of this warp see
+                            uint32_t sc[16], t[16];
+                            tmem_ld16(tmem + C::TM_S + 16 * pc + lanes, sc);
+                            tmem_ld16(tmem + C::TM_T + 16 * pc + lanes, t);
                             tmem_ld_wait();
-                            float w[32];
-                            const int seen = cc < q ? 32 : lane;  // columns before this row
+                            float w[16];
+                            const int seen = i - 16 * pc;      // columns before this row
 #pragma unroll
-                            for (int y = 0; y < 32; y += 4) {
-                                const ulonglong2 sj = *reinterpret_cast<const ulonglong2 *>(&sG[32 * cc + y]);
+                            for (int y = 0; y < 16; y += 4) {
+                                const ulonglong2 sj = *reinterpret_cast<const ulonglong2 *>(&sG[16 * pc + y]);
 #pragma unroll
                                 for (int z = 0; z < 4; z += 2) {
                                     const uint64_t d = ex2_f32x2(sub_f32x2(z == 0 ? sj.x : sj.y, s2));
@@ -349,11 +402,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                                     w[y + z + 1] = y + z + 1 < seen ? __uint_as_float(hi) : 0.f;
                                 }
                             }
-                            if (cc == q) {  // columns behind this row, whatever they hold, give 0
+                            if (pc >= 2 * q) {  // columns behind this row, whatever they hold, give 0
 #pragma unroll
-                                for (int y = 0; y < 16; ++y) {
-                                    const uint32_t mask = 2 * y + 1 <= lane ? 0xffffffffu
-                                                          : 2 * y <= lane   ? 0x0000ffffu
+                                for (int y = 0; y < 8; ++y) {
+                                    const uint32_t mask = 2 * y + 1 <= seen ? 0xffffffffu
+                                                          : 2 * y <= seen   ? 0x0000ffffu
                                                                             : 0u;
                                     P[y] &= mask;
                                     dP[y] &= mask;
@@ -361,29 +414,42 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             }
                             float r0 = 0.f, r1 = 0.f;
 #pragma unroll
-                            for (int y = 0; y < 32; y += 2) r0 += w[y], r1 += w[y + 1];
+                            for (int y = 0; y < 16; y += 2) r0 += w[y], r1 += w[y + 1];
                             row += r0 + r1;
                             col = warp_column_sums(w);
                         } else {
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) P[y] = dP[y] = 0u;
+                            for (int y = 0; y < 8; ++y) P[y] = dP[y] = 0u;
                         }
-                        sCol[128 * q + 32 * cc + lane] = col;
-                        const uint32_t at = sbase + (uint32_t)((cc >> 1) * C::BOX + i * 128);
+                        if (lane < 16) sCol[128 * q + 16 * pc + lane] = col;
+                        const uint32_t at = sbase + (uint32_t)((pc >> 2) * C::BOX + i * 128);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t o = at + (((4 * (cc & 1) + c) ^ (i & 7)) << 4);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t o = at + (((2 * (pc & 3) + c) ^ (i & 7)) << 4);
                             st_shared_v4(C::OFF_P + o, P[4 * c], P[4 * c + 1], P[4 * c + 2], P[4 * c + 3]);
                             st_shared_v4(C::OFF_DP + o, dP[4 * c], dP[4 * c + 1], dP[4 * c + 2], dP[4 * c + 3]);
                         }
-                        if (cc == q) {                         // the last columns of s and t that are read
-                            tc_fence_before();
-                            mbar_arrive(&m->s_free);
-                        }
                     }
-                    sRow[i] = row;
+                    tc_fence_before();
+                    mbar_arrive(&m->s_free);
+                    sRow[128 * half + i] = row;
                     fence_proxy_async_smem();
                     mbar_arrive(&m->p_ready);
+                    ok = wwait(&m->dv_full, ph);
+                }
+                // results: dv over dS (k dS has read it), dk over dP
+                if (ok && half < C::DB) {
+                    tc_fence_after();
+                    store(sbase + C::OFF_DS + (warp - 2) * 4096, C::TM_DV2, p.have_ds != 0, wt, &p.tmap_dv, p.dv, half);
+                }
+                if (ok) ok = wwait(&m->out_full, ph);
+                if (ok) {
+                    tc_fence_after();
+                    if (half < C::DB)
+                        store(sbase + C::OFF_DP + (warp - 2) * 4096, C::TM_DK, false, 0.f, &p.tmap_dk, p.dk, half);
+                    staged();
+                    if (lane == 0) mbar_arrive(&m->stage_free);
+                    tc_fence_before();
                 }
             } else {
                 // -------------------------------------------------------- group B: first terms
@@ -391,7 +457,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 if (ok) ok = wwait(&m->gates, ph) && wwait(&m->full_qk, ph) && wwait(&m->first_full, ph);
                 if (ok) {
                     tc_fence_after();
-                    // rows of D accumulators times w; their product with a row of q or k
+                    // rows of accumulators times w; their product with a row of q or k
                     auto scale = [&](uint32_t col, float w, int tile, float &dot) {
 #pragma unroll 1
                         for (int cc = 0; cc < D / 32; ++cc) {
@@ -401,94 +467,42 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
 #pragma unroll
                             for (int y = 0; y < 32; ++y) a[y] = __float_as_uint(w * __uint_as_float(a[y]));
                             tmem_st32(tmem + col + 32 * cc + lanes, a);
-                            if (tile >= 0) {
+                            float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    const int ch = (cc & 1) * 4 + c;
-                                    const uint4 v = ld_shared_v4(sbase + tile + (cc >> 1) * C::BOX + i * 128 +
-                                                                 ((ch ^ (i & 7)) << 4));
-                                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                            for (int c = 0; c < 4; ++c) {
+                                const int ch = (cc & 1) * 4 + c;
+                                const uint4 v = ld_shared_v4(sbase + tile + (cc >> 1) * C::BOX + i * 128 +
+                                                             ((ch ^ (i & 7)) << 4));
+                                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                    for (int z = 0; z < 4; ++z) {
-                                        dot = fmaf(__uint_as_float(in[z] << 16), __uint_as_float(a[8 * c + 2 * z]), dot);
-                                        dot = fmaf(__uint_as_float(in[z] & 0xffff0000u),
-                                                   __uint_as_float(a[8 * c + 2 * z + 1]), dot);
-                                    }
+                                for (int z = 0; z < 4; ++z) {
+                                    d0 = fmaf(__uint_as_float(in[z] << 16), __uint_as_float(a[8 * c + 2 * z]), d0);
+                                    d1 = fmaf(__uint_as_float(in[z] & 0xffff0000u),
+                                              __uint_as_float(a[8 * c + 2 * z + 1]), d1);
                                 }
                             }
+                            dot += d0 + d1;
                         }
                     };
-                    float none = 0.f;
-                    const float wt = ex2(sG[i]), gam = ex2(m->sum - sG[i]);  // e^{G_C - G_i}, e^{G_i}
-                    if (p.have_s) scale(C::TM_DQ, gam, C::OFF_Q, r);
-                    if (p.have_ds) scale(C::TM_DK, wt, C::OFF_K, e);
+                    // e^{G_i}, e^{G_C - G_i}
+                    if (p.have_s) scale(C::TM_DQ, ex2(m->sum - sG[i]), C::OFF_Q, r);
+                    if (p.have_ds) scale(C::TM_DK, ex2(sG[i]), C::OFF_K, e);
                     sR[i] = r;
                     sE[i] = e;
-                    ok = wwait(&m->dv_full, ph);
-                    if (ok) {
-                        tc_fence_after();
-                        if (p.have_ds) scale(C::TM_DV, wt, -1, none);
-                        tmem_st_wait();
-                        tc_fence_before();
-                        mbar_arrive(&m->scaled);
-                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&m->scaled);
+                    ok = wwait(&m->out_full, ph);
                 }
-            }
-            // ------------------------------------------------------------ results
-            if (ok) ok = wwait(&m->out_full, ph);
-            if (ok) {
-                tc_fence_after();
-                // A box of 64 columns goes through this warp's staging place `slot` to global memory.
-                // (Stores from registers would touch 32 rows each: 32 passes of the memory pipe.)
-                const uint32_t stage = sbase + C::OFF_STAGE + (warp - 2) * 8192;
-                auto store = [&](int slot, uint32_t col, const CUtensorMap *map, __nv_bfloat16 *out, int box) {
-                    const uint32_t to = stage + slot * 4096;
+                if (ok) {
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < 2; ++cc) {
-                        uint32_t a[32];
-                        tmem_ld32(tmem + col + 64 * box + 32 * cc + lanes, a);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            st_shared_v4(to + lane * 128 + (((4 * cc + y) ^ (lane & 7)) << 4),
-                                         pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
-                                         pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
-                                         pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
-                                         pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                    for (int n = 0; n < C::DB; ++n) {
+                        staged();
+                        store(sbase + C::OFF_STAGE + q * 4096, C::TM_DQ, false, 0.f, &p.tmap_dq, p.dq, n);
                     }
-                    if (32 * q + 32 <= nv) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(map, to, h * D + 64 * box, row0 + 32 * q);
-                            bulk_commit_group();
-                        }
-                    } else if (i < nv) {  // the sequence's last rows, one lane each
-                        uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(row0 + i) * p.H + h) * D + 64 * box);
-#pragma unroll 1
-                        for (int z = 0; z < 8; ++z) dst[z] = ld_shared_v4(to + lane * 128 + ((z ^ (lane & 7)) << 4));
-                    }
-                };
-                // group A: dk and (D = 128) dv's second half; group B: dq and dv's first half
-                const bool A = warp < 6;
-                const int boxes = D == 128 ? 3 : A ? 1 : 2;
-#pragma unroll 1
-                for (int n = 0; n < boxes; ++n) {
-                    const bool dv = n == D / 64;
-                    if (n == 2) {
-                        if (lane == 0) bulk_wait_read_all();
-                        __syncwarp();
-                    }
-                    store(n & 1, dv ? C::TM_DV : A ? C::TM_DK : C::TM_DQ,
-                          dv ? &p.tmap_dv : A ? &p.tmap_dk : &p.tmap_dq, dv ? p.dv : A ? p.dk : p.dq,
-                          dv ? (D == 128 && A ? 1 : 0) : n);
+                    tc_fence_before();
                 }
-                if (lane == 0) {
-                    bulk_wait_read_all();
-                    mbar_arrive(&m->stage_free);
-                }
-                __syncwarp();
-                tc_fence_before();
             }
         }
         if (!ok) fail();
