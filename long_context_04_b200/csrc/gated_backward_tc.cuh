@@ -15,7 +15,7 @@
 // two terms of dv take the places of s and t.  The decays of the first terms differ by row:
 // those of dq and dk are scaled in TMEM and the second products accumulate on top, the two of
 // dv are added on the way out.  Eight products, in this order:
-//   s, t; do S^T, v dS^T  ->  P, dP; scaling  ->  k dS; P^T do; dP^T q, dP k.
+//   s, t; do S^T, v dS^T  ->  P, dP; scaling  ->  k dS; P^T do; dP k; dP^T q.
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
@@ -57,8 +57,8 @@ struct GatedBackwardCfg {
     static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
     static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
     static constexpr int OFF_DP = OFF_S;
-    // staging boxes of 64 columns x 32 rows: dv over dS and dk over dP (eight warps of group A),
-    // dq beside them (group B)
+    // staging boxes of 64 columns x 32 rows: dv, then dk over dS (eight warps of group A), dq
+    // beside them (group B)
     static constexpr int OFF_STAGE = OFF_S + 2 * PT + (D == 128 ? 0 : PT);
     static constexpr int OFF_F = OFF_STAGE + 4 * 4096;          // 9 arrays of 128 floats
     static constexpr int OFF_MISC = OFF_F + 9 * 512;
@@ -74,13 +74,13 @@ struct GatedBackwardCfg {
 };
 
 struct GatedBackwardMisc {
-    uint64_t full_qk, full_vo, full_ss;   // tiles landed
+    uint64_t full_qk, full_vo, full_s, full_ds;  // tiles landed
     uint64_t gates;                       // gate sums of the block written
     uint64_t first_full;                  // s, t, do S^T, v dS^T
     uint64_t s_free;                      // group A has read s and t
     uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
-    uint64_t dv_full, out_full;           // dv; dq and dk
-    uint64_t stage_free;                  // group A's results have left the places of S and dS
+    uint64_t dv_full, dq_full, out_full;  // dv; dq; dk, and with it every product
+    uint64_t stage_free;                  // group A's results have left the place of dS
     uint64_t done;
     float sum;                            // log-decay of the block, times log2(e)
     uint32_t tmem_base;
@@ -124,10 +124,12 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     if (tid == 0) {
         mbar_init(&m->full_qk, 1);
         mbar_init(&m->full_vo, 1);
-        mbar_init(&m->full_ss, 1);
+        mbar_init(&m->full_s, 1);
+        mbar_init(&m->full_ds, 1);
         mbar_init(&m->gates, 32);
         mbar_init(&m->first_full, 1);
         mbar_init(&m->dv_full, 1);
+        mbar_init(&m->dq_full, 1);
         mbar_init(&m->s_free, C::GROUP_A);
         mbar_init(&m->p_ready, C::GROUP_A);
         mbar_init(&m->scaled, C::GROUP_B);
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
-    // Loads of tile x, by a whole warp; the states' part apart, into the results' staging place.
+    // Loads of tile x, by a whole warp; dS apart, which goes to group A's staging place.
     int loads = 0, state_loads = 0;
     auto load_tiles = [&](int x) {
         int rank, blk, start, len, sid;
@@ -177,16 +179,18 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             tma_load_2d(sbase + C::OFF_DO + d * C::BOX, &p.tmap_do, col + 64 * d, row, &m->full_vo);
             tma_load_2d(sbase + C::OFF_V + d * C::BOX, &p.tmap_v, col + 64 * d, row, &m->full_vo);
         }
+        mbar_arrive_expect_tx(&m->full_s, p.have_s * C::DB * C::SBOX);
+#pragma unroll 1
+        for (int d = 0; d < C::DB * p.have_s; ++d)
+            tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_s);
     };
     auto load_states = [&](int x) {
         ++state_loads;
         if (lane != 0) return;
-        mbar_arrive_expect_tx(&m->full_ss, (p.have_s + p.have_ds) * C::DB * C::SBOX);
+        mbar_arrive_expect_tx(&m->full_ds, p.have_ds * C::DB * C::SBOX);
 #pragma unroll 1
-        for (int d = 0; d < C::DB; ++d) {
-            if (p.have_s) tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_ss);
-            if (p.have_ds) tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ss);
-        }
+        for (int d = 0; d < C::DB * p.have_ds; ++d)
+            tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ds);
     };
     uint32_t raw[4];  // gates of the next tile, fetched ahead (warp 0)
     auto fetch = [&](int x) {
@@ -257,12 +261,16 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             if (ok) {
                 tc_fence_after();
                 product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
-                ok = wwait(&m->full_ss, ph);
+                ok = wwait(&m->full_s, ph);
             }
             if (ok) {
                 tc_fence_after();
                 if (p.have_s)
                     product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
+                ok = wwait(&m->full_ds, ph);
+            }
+            if (ok) {
+                tc_fence_after();
                 if (p.have_ds)
                     product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
                 warp_commit(leader, &m->first_full);
@@ -286,10 +294,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             }
             if (ok) {
                 tc_fence_after();
-                product(C::TM_DK, desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX), nn,
-                        desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
                 product(C::TM_DQ, desc_kmajor_sw128(sbase + C::OFF_DP), kk, desc_mnmajor_sw128(sbase + C::OFF_K, C::BOX),
                         nn, C::ID_KN, C::C / 16, p.have_s != 0);
+                warp_commit(leader, &m->dq_full);
+                product(C::TM_DK, desc_mnmajor_sw128(sbase + C::OFF_DP, C::BOX), nn,
+                        desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
                 warp_commit(leader, &m->out_full);
             }
             if (ok && p.dg != nullptr) {
@@ -327,21 +336,21 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             auto store = [&](uint32_t stage, uint32_t col, bool twice, float w, const CUtensorMap *map,
                              __nv_bfloat16 *out, int box) {
 #pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t a[16];
-                    tmem_ld16(tmem + col + 64 * box + 16 * cc + lanes, a);
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t a[32];
+                    tmem_ld32(tmem + col + 64 * box + 32 * cc + lanes, a);
                     if (twice) {
-                        uint32_t c[16];
-                        tmem_ld16(tmem + C::TM_DV1 + 64 * box + 16 * cc + lanes, c);
+                        uint32_t c[32];
+                        tmem_ld32(tmem + C::TM_DV1 + 64 * box + 32 * cc + lanes, c);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
+                        for (int y = 0; y < 32; ++y)
                             a[y] = __float_as_uint(fmaf(w, __uint_as_float(c[y]), __uint_as_float(a[y])));
                     }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        st_shared_v4(stage + lane * 128 + (((2 * cc + y) ^ (lane & 7)) << 4),
+                    for (int y = 0; y < 4; ++y)
+                        st_shared_v4(stage + lane * 128 + (((4 * cc + y) ^ (lane & 7)) << 4),
                                      pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
                                      pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
                                      pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
@@ -384,8 +393,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             tmem_ld16(tmem + C::TM_S + 16 * pc + lanes, sc);
                             tmem_ld16(tmem + C::TM_T + 16 * pc + lanes, t);
                             tmem_ld_wait();
-                            float w[16];
-                            const int seen = i - 16 * pc;      // columns before this row
+                            uint64_t w2[8], sum2 = 0;          // W in pairs of columns
 #pragma unroll
                             for (int y = 0; y < 16; y += 4) {
                                 const ulonglong2 sj = *reinterpret_cast<const ulonglong2 *>(&sG[16 * pc + y]);
@@ -396,26 +404,29 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                                     const uint64_t pp = mul_f32x2(pair_f32(sc[y + z], sc[y + z + 1]), d);
                                     P[(y + z) / 2] = pack_f32x2(pp);
                                     dP[(y + z) / 2] = pack_f32x2(mul_f32x2(tt, d));
-                                    uint32_t lo, hi;
-                                    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(mul_f32x2(pp, tt)));
-                                    w[y + z] = y + z < seen ? __uint_as_float(lo) : 0.f;
-                                    w[y + z + 1] = y + z + 1 < seen ? __uint_as_float(hi) : 0.f;
+                                    w2[(y + z) / 2] = mul_f32x2(pp, tt);
                                 }
                             }
                             if (pc >= 2 * q) {  // columns behind this row, whatever they hold, give 0
+                                const int seen = i - 16 * pc;  // columns before this row
 #pragma unroll
                                 for (int y = 0; y < 8; ++y) {
-                                    const uint32_t mask = 2 * y + 1 <= seen ? 0xffffffffu
-                                                          : 2 * y <= seen   ? 0x0000ffffu
-                                                                            : 0u;
-                                    P[y] &= mask;
-                                    dP[y] &= mask;
+                                    const uint32_t m0 = 2 * y <= seen ? 0xffffffffu : 0u,
+                                                   m1 = 2 * y + 1 <= seen ? 0xffffffffu : 0u,
+                                                   m2 = 2 * y + 2 <= seen ? 0xffffffffu : 0u;
+                                    P[y] &= (m0 & 0xffffu) | (m1 & 0xffff0000u);
+                                    dP[y] &= (m0 & 0xffffu) | (m1 & 0xffff0000u);
+                                    w2[y] &= (uint64_t)m1 | ((uint64_t)m2 << 32);  // j < i
                                 }
                             }
-                            float r0 = 0.f, r1 = 0.f;
+                            float w[16];
 #pragma unroll
-                            for (int y = 0; y < 16; y += 2) r0 += w[y], r1 += w[y + 1];
-                            row += r0 + r1;
+                            for (int y = 0; y < 8; ++y) {
+                                sum2 = add_f32x2(sum2, w2[y]);
+                                w[2 * y] = __uint_as_float((uint32_t)w2[y]);
+                                w[2 * y + 1] = __uint_as_float((uint32_t)(w2[y] >> 32));
+                            }
+                            row += __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
                             col = warp_column_sums(w);
                         } else {
 #pragma unroll
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                     mbar_arrive(&m->p_ready);
                     ok = wwait(&m->dv_full, ph);
                 }
-                // results: dv over dS (k dS has read it), dk over dP
+                // results, over dS (k dS has read it)
                 if (ok && half < C::DB) {
                     tc_fence_after();
                     store(sbase + C::OFF_DS + (warp - 2) * 4096, C::TM_DV2, p.have_ds != 0, wt, &p.tmap_dv, p.dv, half);
@@ -445,8 +456,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 if (ok) ok = wwait(&m->out_full, ph);
                 if (ok) {
                     tc_fence_after();
+                    staged();
                     if (half < C::DB)
-                        store(sbase + C::OFF_DP + (warp - 2) * 4096, C::TM_DK, false, 0.f, &p.tmap_dk, p.dk, half);
+                        store(sbase + C::OFF_DS + (warp - 2) * 4096, C::TM_DK, false, 0.f, &p.tmap_dk, p.dk, half);
                     staged();
                     if (lane == 0) mbar_arrive(&m->stage_free);
                     tc_fence_before();
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&m->scaled);
-                    ok = wwait(&m->out_full, ph);
+                    ok = wwait(&m->dq_full, ph);
                 }
                 if (ok) {
                     tc_fence_after();
@@ -517,8 +529,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         if (loads > 0) {
             mbar_wait(&m->full_qk, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
             mbar_wait(&m->full_vo, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
+            mbar_wait(&m->full_s, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
         }
-        if (state_loads > 0) mbar_wait(&m->full_ss, (uint32_t)((state_loads - 1) & 1), nullptr, tlimit);
+        if (state_loads > 0) mbar_wait(&m->full_ds, (uint32_t)((state_loads - 1) & 1), nullptr, tlimit);
     }
     if (warp >= 2 && lane == 0) bulk_wait_all();
     if (warp == 1) {  // every issued MMA has finished before TMEM is freed

@@ -147,10 +147,15 @@ __device__ __forceinline__ float suffix_gates4(const float (&x)[4], float (&sum)
     return __shfl_sync(0xffffffffu, run, 0);
 }
 
-// Products and differences of fp32 pairs.
+// Products, sums and differences of fp32 pairs.
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f32x2(uint64_t x) {  // two fp32 values as a bf16 pair
