@@ -10,8 +10,7 @@
 //   terms.
 //
 // A persistent CTA per SM.  Shared memory (D = 128): q, k, v, do 32 KB each, S and dS 32 KB
-// each; P takes the place of v and dP that of S once the products that read those are done,
-// and results are staged over S and dS on their way out.  TMEM, 512 columns: s, t, dq, dk; the
+// each; P takes the place of v and dP that of S once the products that read those are done.  TMEM, 512 columns: s, t, dq, dk; the
 // two terms of dv take the places of s and t.  The decays of the first terms differ by row:
 // those of dq and dk are scaled in TMEM and the second products accumulate on top, the two of
 // dv are added on the way out.  Eight products, in this order:
@@ -22,7 +21,8 @@
 // Warps: 0 TMA loads and gate sums; 1 MMA issue and dg; 2-9 (group A) scores -> P, dP, W, then
 // dv and dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out.
 // Every barrier completes one phase per block, and all warps meet at the block's end; the
-// next block's tiles are loaded while the results go out.
+// next block's tiles are fetched into L2 while this one computes and loaded while its results
+// go out.
 //
 // HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head
 // (2304 at D = 128); tensor: 8 products of 512 cycles per block.
@@ -35,7 +35,6 @@ namespace la {
 struct GatedBackwardParams {
     CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;  // [T][H*D], box 64 x 128
     CUtensorMap tmap_s, tmap_ds;                  // [blocks * H * D][D], box 64 x D
-    CUtensorMap tmap_dq, tmap_dk, tmap_dv;        // results, box 64 x 32
     const __nv_bfloat16 *g;
     const float *through;  // [blocks][H][4 D / 64] parts of e^{G_C} <dS, S>, or nullptr
     __nv_bfloat16 *dq, *dk, *dv, *dg;
@@ -57,10 +56,7 @@ struct GatedBackwardCfg {
     static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
     static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
     static constexpr int OFF_DP = OFF_S;
-    // staging boxes of 64 columns x 32 rows: dv, then dk over dS (eight warps of group A), dq
-    // beside them (group B)
-    static constexpr int OFF_STAGE = OFF_S + 2 * PT + (D == 128 ? 0 : PT);
-    static constexpr int OFF_F = OFF_STAGE + 4 * 4096;          // 9 arrays of 128 floats
+    static constexpr int OFF_F = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 9 arrays of 128 floats
     static constexpr int OFF_MISC = OFF_F + 9 * 512;
     static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
     static_assert(DB * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
@@ -74,13 +70,12 @@ struct GatedBackwardCfg {
 };
 
 struct GatedBackwardMisc {
-    uint64_t full_qk, full_vo, full_s, full_ds;  // tiles landed
+    uint64_t full_qk, full_vo, full_ss;   // tiles landed
     uint64_t gates;                       // gate sums of the block written
     uint64_t first_full;                  // s, t, do S^T, v dS^T
     uint64_t s_free;                      // group A has read s and t
     uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
     uint64_t dv_full, dq_full, out_full;  // dv; dq; dk, and with it every product
-    uint64_t stage_free;                  // group A's results have left the place of dS
     uint64_t done;
     float sum;                            // log-decay of the block, times log2(e)
     uint32_t tmem_base;
@@ -124,8 +119,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     if (tid == 0) {
         mbar_init(&m->full_qk, 1);
         mbar_init(&m->full_vo, 1);
-        mbar_init(&m->full_s, 1);
-        mbar_init(&m->full_ds, 1);
+        mbar_init(&m->full_ss, 1);
         mbar_init(&m->gates, 32);
         mbar_init(&m->first_full, 1);
         mbar_init(&m->dv_full, 1);
@@ -134,7 +128,6 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         mbar_init(&m->p_ready, C::GROUP_A);
         mbar_init(&m->scaled, C::GROUP_B);
         mbar_init(&m->out_full, 1);
-        mbar_init(&m->stage_free, 8);
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
         fence_mbarrier_init_cluster();
@@ -158,9 +151,8 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
-    // Loads of tile x, by a whole warp; dS apart, which goes to group A's staging place.
-    int loads = 0, state_loads = 0;
-    auto load_tiles = [&](int x) {
+    int loads = 0;
+    auto load_tiles = [&](int x) {  // by a whole warp
         int rank, blk, start, len, sid;
         p.tab.block(x / p.H, rank, blk);
         p.tab.seqs.get(rank, start, len, sid);
@@ -168,29 +160,41 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         ++loads;
         if (lane != 0) return;
         mbar_arrive_expect_tx(&m->full_qk, 2 * C::TILE);
+        mbar_arrive_expect_tx(&m->full_vo, 2 * C::TILE);
+        mbar_arrive_expect_tx(&m->full_ss, (p.have_s + p.have_ds) * C::DB * C::SBOX);
 #pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
             tma_load_2d(sbase + C::OFF_Q + d * C::BOX, &p.tmap_q, col + 64 * d, row, &m->full_qk);
             tma_load_2d(sbase + C::OFF_K + d * C::BOX, &p.tmap_k, col + 64 * d, row, &m->full_qk);
         }
-        mbar_arrive_expect_tx(&m->full_vo, 2 * C::TILE);
 #pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
             tma_load_2d(sbase + C::OFF_DO + d * C::BOX, &p.tmap_do, col + 64 * d, row, &m->full_vo);
             tma_load_2d(sbase + C::OFF_V + d * C::BOX, &p.tmap_v, col + 64 * d, row, &m->full_vo);
         }
-        mbar_arrive_expect_tx(&m->full_s, p.have_s * C::DB * C::SBOX);
 #pragma unroll 1
-        for (int d = 0; d < C::DB * p.have_s; ++d)
-            tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_s);
+        for (int d = 0; d < C::DB; ++d) {
+            if (p.have_s) tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_ss);
+            if (p.have_ds) tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ss);
+        }
     };
-    auto load_states = [&](int x) {
-        ++state_loads;
+    // The next tile's data into L2 while this one computes: shared memory is full, so that its
+    // loads can only start when this tile's last product is done.
+    auto prefetch = [&](int x) {
+        int rank, blk, start, len, sid;
+        p.tab.block(x / p.H, rank, blk);
+        p.tab.seqs.get(rank, start, len, sid);
+        const int row = start + blk * C::C, col = (x % p.H) * D;
         if (lane != 0) return;
-        mbar_arrive_expect_tx(&m->full_ds, p.have_ds * C::DB * C::SBOX);
 #pragma unroll 1
-        for (int d = 0; d < C::DB * p.have_ds; ++d)
-            tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ds);
+        for (int d = 0; d < C::DB; ++d) {
+            tma_prefetch_l2_2d(&p.tmap_q, col + 64 * d, row);
+            tma_prefetch_l2_2d(&p.tmap_k, col + 64 * d, row);
+            tma_prefetch_l2_2d(&p.tmap_do, col + 64 * d, row);
+            tma_prefetch_l2_2d(&p.tmap_v, col + 64 * d, row);
+            if (p.have_s) tma_prefetch_l2_2d(&p.tmap_s, 64 * d, x * D);
+            if (p.have_ds) tma_prefetch_l2_2d(&p.tmap_ds, 64 * d, x * D);
+        }
     };
     uint32_t raw[4];  // gates of the next tile, fetched ahead (warp 0)
     auto fetch = [&](int x) {
@@ -201,7 +205,6 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     };
     if (warp == 0 && (int)blockIdx.x < tiles) {
         load_tiles(blockIdx.x);
-        load_states(blockIdx.x);
         fetch(blockIdx.x);
     }
     const uint32_t leader = elect_leader();
@@ -229,11 +232,12 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             widen_gates4(gate, raw);
             store_gate_sums(sG, &m->sum, gate);
             mbar_arrive(&m->gates);
-            if (next < tiles) fetch(next);
+            if (next < tiles) {
+                fetch(next);
+                prefetch(next);
+            }
             if (ok) ok = wwait(&m->out_full, ph);
             if (ok && next < tiles) load_tiles(next);  // every product that reads the tiles is done
-            if (ok) ok = wwait(&m->stage_free, ph);
-            if (ok && next < tiles) load_states(next);
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
@@ -261,16 +265,12 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             if (ok) {
                 tc_fence_after();
                 product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
-                ok = wwait(&m->full_s, ph);
+                ok = wwait(&m->full_ss, ph);
             }
             if (ok) {
                 tc_fence_after();
                 if (p.have_s)
                     product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
-                ok = wwait(&m->full_ds, ph);
-            }
-            if (ok) {
-                tc_fence_after();
                 if (p.have_ds)
                     product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
                 warp_commit(leader, &m->first_full);
@@ -330,48 +330,37 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             const uint32_t lanes = (uint32_t)(32 * q) << 16;
             const bool A = warp < 2 + C::GROUP_A / 32;
             const int half = A ? (warp - 2) >> 2 : 0;
-            // A box of 64 columns, times w where `twice` adds a second accumulator, goes through this
-            // warp's staging place to global memory.  (Stores from registers would touch 32 rows
-            // each: 32 passes of the memory pipe.)
-            auto store = [&](uint32_t stage, uint32_t col, bool twice, float w, const CUtensorMap *map,
-                             __nv_bfloat16 *out, int box) {
-#pragma unroll 1
-                for (int cc = 0; cc < 2; ++cc) {
-                    uint32_t a[32];
-                    tmem_ld32(tmem + col + 64 * box + 32 * cc + lanes, a);
+            // 64 columns of this warp's rows out of TMEM and into `out`; with `twice`, dv's first
+            // term times w is added.
+            auto store = [&](uint32_t col, bool twice, float w, __nv_bfloat16 *out, int box) {
+                uint4 c[8];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t a[16];
+                    tmem_ld16(tmem + col + 64 * box + 16 * x + lanes, a);
                     if (twice) {
-                        uint32_t c[32];
-                        tmem_ld32(tmem + C::TM_DV1 + 64 * box + 32 * cc + lanes, c);
+                        uint32_t b[16];
+                        tmem_ld16(tmem + C::TM_DV1 + 64 * box + 16 * x + lanes, b);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            a[y] = __float_as_uint(fmaf(w, __uint_as_float(c[y]), __uint_as_float(a[y])));
+                        for (int y = 0; y < 16; ++y)
+                            a[y] = __float_as_uint(fmaf(w, __uint_as_float(b[y]), __uint_as_float(a[y])));
                     }
                     tmem_ld_wait();
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        st_shared_v4(stage + lane * 128 + (((4 * cc + y) ^ (lane & 7)) << 4),
-                                     pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                    for (int y = 0; y < 2; ++y)
+                        c[2 * x + y] =
+                            make_uint4(pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
+                                       pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
+                                       pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
+                                       pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
                 }
-                if (32 * q + 32 <= nv) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(map, stage, h * D + 64 * box, row0 + 32 * q);
-                        bulk_commit_group();
-                    }
-                } else if (i < nv) {  // the sequence's last rows, one lane each
-                    uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(row0 + i) * p.H + h) * D + 64 * box);
-#pragma unroll 1
-                    for (int z = 0; z < 8; ++z) dst[z] = ld_shared_v4(stage + lane * 128 + ((z ^ (lane & 7)) << 4));
-                }
-            };
-            auto staged = [&]() {  // the warp's staging places may be written again
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
+                transpose_chunks(c);
+                const int r0 = i & ~7;
+                __nv_bfloat16 *dst = out + ((size_t)(row0 + r0) * p.H + h) * D + 64 * box + 8 * (lane & 7);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (r0 + x < nv) *reinterpret_cast<uint4 *>(dst + (size_t)x * p.H * D) = c[x];
             };
             if (A) {
                 // -------------------------------------------------------- group A: P, dP, W
@@ -448,19 +437,14 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                     mbar_arrive(&m->p_ready);
                     ok = wwait(&m->dv_full, ph);
                 }
-                // results, over dS (k dS has read it)
-                if (ok && half < C::DB) {
+                // results: dv while the products of dq and dk run, then dk
+#pragma unroll 1
+                for (int n = 0; n < 2; ++n) {
+                    if (ok && n == 1) ok = wwait(&m->out_full, ph);
+                    if (!ok) break;
                     tc_fence_after();
-                    store(sbase + C::OFF_DS + (warp - 2) * 4096, C::TM_DV2, p.have_ds != 0, wt, &p.tmap_dv, p.dv, half);
-                }
-                if (ok) ok = wwait(&m->out_full, ph);
-                if (ok) {
-                    tc_fence_after();
-                    staged();
                     if (half < C::DB)
-                        store(sbase + C::OFF_DS + (warp - 2) * 4096, C::TM_DK, false, 0.f, &p.tmap_dk, p.dk, half);
-                    staged();
-                    if (lane == 0) mbar_arrive(&m->stage_free);
+                        store(n == 0 ? C::TM_DV2 : C::TM_DK, n == 0 && p.have_ds != 0, wt, n == 0 ? p.dv : p.dk, half);
                     tc_fence_before();
                 }
             } else {
@@ -509,10 +493,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 if (ok) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int n = 0; n < C::DB; ++n) {
-                        staged();
-                        store(sbase + C::OFF_STAGE + q * 4096, C::TM_DQ, false, 0.f, &p.tmap_dq, p.dq, n);
-                    }
+                    for (int n = 0; n < C::DB; ++n) store(C::TM_DQ, false, 0.f, p.dq, n);
                     tc_fence_before();
                 }
             }
@@ -529,11 +510,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         if (loads > 0) {
             mbar_wait(&m->full_qk, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
             mbar_wait(&m->full_vo, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
-            mbar_wait(&m->full_s, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
+            mbar_wait(&m->full_ss, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
         }
-        if (state_loads > 0) mbar_wait(&m->full_ds, (uint32_t)((state_loads - 1) & 1), nullptr, tlimit);
     }
-    if (warp >= 2 && lane == 0) bulk_wait_all();
     if (warp == 1) {  // every issued MMA has finished before TMEM is freed
         warp_commit(leader, &m->done);
         mbar_wait(&m->done, 0u, nullptr, tlimit);

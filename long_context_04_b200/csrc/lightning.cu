@@ -442,8 +442,7 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
     if (!make_map(&p.tmap_q, q, T, H, D, C::C) || !make_map(&p.tmap_k, k, T, H, D, C::C) ||
         !make_map(&p.tmap_v, v, T, H, D, C::C) || !make_map(&p.tmap_do, dout, T, H, D, C::C) ||
         (snap != nullptr && !make_map(&p.tmap_s, snap, rows, 1, D, D)) ||
-        (dsnap != nullptr && !make_map(&p.tmap_ds, dsnap, rows, 1, D, D)) || !make_map(&p.tmap_dq, dq, T, H, D, 32) ||
-        !make_map(&p.tmap_dk, dk, T, H, D, 32) || !make_map(&p.tmap_dv, dv, T, H, D, 32))
+        (dsnap != nullptr && !make_map(&p.tmap_ds, dsnap, rows, 1, D, D)))
         return LA_ERR_CUDA;
     p.g = static_cast<const bf *>(g);
     p.through = through;
