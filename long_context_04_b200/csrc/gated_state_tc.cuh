@@ -7,16 +7,22 @@
 // per block, from which the block kernels then run independently of each other.
 //
 // One CTA per (segment, head, 64-column slice of the state).  Per block the tile of the left
-// factor (128 x D) and the slice of the right one (128 x 64) arrive by TMA; six warps scale
+// factor (128 x D) and the slice of the right one (128 x 64) arrive by TMA; eight warps scale
 // the slice's rows by their decays and split every product into three bf16 numbers whose sum
 // is the fp32 product to 2^-26 (one bf16 alone would round the state by 2^-9 in every step);
 // one warp issues the product of the tile with the first two parts side by side (one read of
 // the left factor from shared memory for both) and adds that with the third to the second's
-// columns; the epilogue adds the two accumulators to the fp32 state in its registers.
+// columns, a quarter of the tokens at a time as they are scaled; the epilogue adds the two
+// accumulators to the fp32 state in its registers and stores the snapshots by TMA.
 //
 // The tensor work (3 x 2 D^2 flops per token) is below its HBM time: 4 D bytes read (the left
 // tile is read by D / 64 CTAs, mostly from L2) and 2 D^2 / 128 bytes of snapshot written per
 // token and head.
+//
+// Warpgroups (512 threads; registers are moved to the one that holds the state):
+//   0  warp 0 TMA loads and gate sums; warp 1 MMA issue
+//   1  epilogue: the state, its snapshots, in the reverse scan the parts of e^{G_C} <X, state>
+//   2, 3  scaling
 #pragma once
 
 #include "gated.cuh"
@@ -32,46 +38,66 @@ struct GatedStateParams {
     float *seg_out;             // [segs][H][D][D]: a segment's own end state, or nullptr
     float *seg_total;           // [segs][H]: its summed log-decay
     float *fin;                 // [S][H][D][D] or nullptr: final states
-    __nv_bfloat16 *snap;        // [blocks][H][D][D] or nullptr
-    const __nv_bfloat16 *other; // reverse: the forward snapshots, or nullptr
-    float *through;             // reverse: [blocks][H][4 D / 64] parts of e^{G_C} <X, state>
+    CUtensorMap tmap_snap;      // snapshots, [blocks * H * D][D], box 64 x D
+    CUtensorMap tmap_other;     // reverse: the forward snapshots, the same
+    int have_snap;
+    float *through;             // reverse: [blocks][H][4 D / 64] parts of e^{G_C} <X, state>, or nullptr
     int H;
     unsigned long long timeout_ns;
     GatedTable tab;
 };
 
-template <int D>
+template <int D, bool REV>
 struct GatedStateCfg {
     static constexpr int C = 128;
     static constexpr int NVS = D / 64;              // column slices (CTAs) per (segment, head)
     static constexpr int DB = D / 64;               // 64-column boxes of the left tile
     static constexpr int BOX = C * 128;             // 128 rows x 128 B
+    static constexpr int SBOX = D * 128;            // a slice of a state's snapshot
     static constexpr int STAGE = (DB + 3) * BOX;    // left tile, then the slice and its two lower parts
     static constexpr int LOADED = (DB + 1) * BOX;
     static constexpr int NST = 2;
-    static constexpr int SCALERS = 6;               // warps (12 in all: 168 registers a thread)
-    static constexpr int OFF_G = NST * STAGE;       // gate sums, two blocks
+    static constexpr int OFF_SNAP = NST * STAGE;    // snapshots on their way out, two
+    static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: forward snapshots, two
+    static constexpr int OFF_G = OFF_OTHER + (REV ? 2 * SBOX : 0);        // gate sums, two blocks
     static constexpr int OFF_MISC = OFF_G + 2 * C * 4;
-    static constexpr int SMEM_USED = 1024 + OFF_MISC + 1024;
+    static constexpr int SMEM_USED = 1024 + OFF_MISC + 512;
     // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
     static constexpr int SMEM_BYTES = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static constexpr int TMEM_COLS = 256;           // two accumulators of 128 columns
     static constexpr int ACC = 128;
-    static constexpr int GROUP = 128;               // epilogue threads
-    static constexpr int THREADS = 64 + GROUP + 32 * SCALERS;
+    static constexpr int GROUP = 128, THREADS = 4 * GROUP;
+    // registers a thread: launched with 128; the shares of the four warpgroups add up to 4 * 128
+    static constexpr int R_LAUNCH = 128, R_MISC = 64, R_STATE = 224, R_SCALE = 112;
+    static_assert(R_MISC + R_STATE + 2 * R_SCALE == 4 * R_LAUNCH, "register shares");
     static constexpr uint32_t ID2 = idesc_bf16_f32(D, 128, 1, 1), ID1 = idesc_bf16_f32(D, 64, 1, 1);
 };
 
 struct GatedStateMisc {
-    uint64_t full[2], ready[2], empty[2];  // tiles landed, scaled, released
+    uint64_t full[2], empty[2];            // tiles landed, released
+    uint64_t ready[2][4];                  // a quarter of the slice scaled
     uint64_t acc_full[2], acc_free[2];
+    uint64_t other_full[2], other_free[2]; // reverse: the forward snapshot of a block
     uint64_t gates_ready[2], gates_free[2];
     uint64_t done;
     float sum[2];          // log-decay of a block, times log2(e)
     uint32_t tmem_base;
     int abort_flag;
 };
+
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Wait until at most one of this thread's committed bulk stores still reads shared memory.
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 
 // A wait of a whole warp for a phase: true once every lane has seen it complete, false after
 // `limit_ns` or once another warp gave up.  Written for few instructions: these kernels run
@@ -325,9 +351,10 @@ __device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4 &v) {
 }
 
 template <int D, bool REV>
-__global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
     gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
-    using C = GatedStateCfg<D>;
+    using C = GatedStateCfg<D, REV>;
+    static_assert(sizeof(GatedStateMisc) <= 512, "misc area");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -341,21 +368,26 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
     p.tab.seqs.get(rank, start, len, sid);
     const int all = (len + C::C - 1) / C::C;
     const int b0 = s * p.tab.seg_blocks, nb = max(0, min(all, b0 + p.tab.seg_blocks) - b0);
+    const int first = p.tab.first_block(rank);
+    const bool through = REV && p.through != nullptr;
     const uint64_t tlimit = p.timeout_ns;
     volatile int *abort_flag = &m->abort_flag;
-    // the t-th block that the scan visits, and its tokens
+    // the t-th block that the scan visits, its tokens, its number (times H, plus h) in the call
     auto block_of = [&](int t) { return REV ? b0 + nb - 1 - t : b0 + t; };
-    auto rows_of = [&](int blk) { return min(C::C, len - blk * C::C); };
+    auto rows_of = [&](int t) { return min(C::C, len - block_of(t) * C::C); };
+    auto number_of = [&](int t) { return (first + block_of(t)) * p.H + h; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->full[i], 1);
-            mbar_init(&m->ready[i], 32 * C::SCALERS);
+            for (int u = 0; u < 4; ++u) mbar_init(&m->ready[i][u], 64);
             mbar_init(&m->empty[i], 1);
             mbar_init(&m->acc_full[i], 1);
             mbar_init(&m->acc_free[i], C::GROUP);
+            mbar_init(&m->other_full[i], 1);
+            mbar_init(&m->other_free[i], C::GROUP);
             mbar_init(&m->gates_ready[i], 32);
-            mbar_init(&m->gates_free[i], C::GROUP / 32 + C::SCALERS);
+            mbar_init(&m->gates_free[i], 12);  // the warps of the epilogue and of scaling
         }
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
@@ -380,69 +412,92 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
     };
     // Every ring has two slots: use t of a slot is its phase t / 2, and a slot is refilled
     // only after its release of use t - 2, so that each wait below sees the phase it means.
+    auto two = [](int t) { return (uint32_t)((t >> 1) & 1); };
     auto stage = [&](int t) { return sbase + (uint32_t)((t & 1) * C::STAGE); };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- TMA loads, gate sums
-        int issued = 0;
-        uint32_t raw[4];
-        float gate[4];
-        if (nb > 0) fetch_gates4(raw, p.g, start + block_of(0) * C::C, rows_of(block_of(0)), p.H, h);
-        for (int t = 0; t < nb; ++t) {
-            if (!wwait(&m->gates_free[t & 1], (uint32_t)(((t >> 1) & 1) ^ 1))) break;
-            widen_gates4(gate, raw);
-            store_gate_sums<REV>(reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (t & 1), &m->sum[t & 1], gate);
-            mbar_arrive(&m->gates_ready[t & 1]);
-            if (t + 1 < nb)
-                fetch_gates4(raw, p.g, start + block_of(t + 1) * C::C, rows_of(block_of(t + 1)), p.H, h);
-            if (!wwait(&m->empty[t & 1], (uint32_t)(((t >> 1) & 1) ^ 1))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&m->full[t & 1], (uint32_t)C::LOADED);
-                const int row = start + block_of(t) * C::C, col = h * D;
+    if (warp < 4) {
+        reg_dec<C::R_MISC>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ TMA loads, gate sums
+            int issued = 0;
+            uint32_t raw[4];
+            float gate[4];
+            auto fetch = [&](int t) {
+                fetch_gates4(raw, p.g, start + block_of(t) * C::C, rows_of(t), p.H, h);
+            };
+            if (nb > 0) fetch(0);
+            for (int t = 0; t < nb; ++t) {
+                if (!wwait(&m->empty[t & 1], two(t) ^ 1u)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&m->full[t & 1], (uint32_t)C::LOADED);
+                    const int row = start + block_of(t) * C::C, col = h * D;
 #pragma unroll
-                for (int d = 0; d < C::DB; ++d)
-                    tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t & 1]);
-                tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t & 1]);
+                    for (int d = 0; d < C::DB; ++d)
+                        tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t & 1]);
+                    tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t & 1]);
+                }
+                if (through) {
+                    if (!wwait(&m->other_free[t & 1], two(t) ^ 1u)) {
+                        // (the tiles of this block are in flight)
+                        mbar_wait(&m->full[t & 1], two(t), nullptr, tlimit);
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&m->other_full[t & 1], (uint32_t)C::SBOX);
+                        tma_load_2d(sbase + C::OFF_OTHER + (t & 1) * C::SBOX, &p.tmap_other, 64 * vs,
+                                    number_of(t) * D, &m->other_full[t & 1]);
+                    }
+                }
+                ++issued;
+                if (!wwait(&m->gates_free[t & 1], two(t) ^ 1u)) break;
+                widen_gates4(gate, raw);
+                store_gate_sums<REV>(reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (t & 1), &m->sum[t & 1], gate);
+                mbar_arrive(&m->gates_ready[t & 1]);
+                if (t + 1 < nb) fetch(t + 1);
             }
-            ++issued;
-        }
-        if (issued < nb) fail();
-        // loads that are still in flight land before the CTA ends
-        for (int t = max(0, issued - 2); t < issued; ++t)
-            mbar_wait(&m->full[t & 1], (uint32_t)((t >> 1) & 1), nullptr, tlimit);
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issuer
-        const uint32_t leader = elect_leader();
-        bool ok = true;
-        for (int t = 0; t < nb; ++t) {
-            if (!wwait(&m->full[t & 1], (uint32_t)((t >> 1) & 1)) ||
-                !wwait(&m->ready[t & 1], (uint32_t)((t >> 1) & 1)) ||
-                (t >= 2 && !wwait(&m->acc_free[t & 1], (uint32_t)(((t - 2) >> 1) & 1)))) {
-                ok = false;
-                break;
+            if (issued < nb || *abort_flag) fail();
+            // loads that are still in flight land before the CTA ends
+            for (int t = max(0, issued - 2); t < issued; ++t) {
+                mbar_wait(&m->full[t & 1], two(t), nullptr, tlimit);
+                if (through) mbar_wait(&m->other_full[t & 1], two(t), nullptr, tlimit);
             }
-            tc_fence_after();
-            // [dims][2 x 64 columns] = A^T [part 0 | part 1 + part 2]
-            const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
-            const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
-#pragma unroll 2
-            for (int ks = 0; ks < C::C / 16; ++ks)
-                warp_mma_ss(leader, tmem + C::ACC * (t & 1), desc_add(ad, ks * 2048), desc_add(bd, ks * 2048), C::ID2,
-                            ks > 0 ? 1u : 0u);
-#pragma unroll 2
-            for (int ks = 0; ks < C::C / 16; ++ks)
-                warp_mma_ss(leader, tmem + C::ACC * (t & 1) + 64, desc_add(ad, ks * 2048),
-                            desc_add(bd, 2 * C::BOX + ks * 2048), C::ID1, 1u);
-            warp_commit(leader, &m->empty[t & 1]);
-            warp_commit(leader, &m->acc_full[t & 1]);
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issue
+            const uint32_t leader = elect_leader();
+            bool ok = true;
+            for (int t = 0; ok && t < nb; ++t) {
+                ok = wwait(&m->full[t & 1], two(t)) && (t < 2 || wwait(&m->acc_free[t & 1], two(t - 2)));
+                // [dims][2 x 64 columns] = A^T [part 0 | part 1 + part 2]
+                const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
+                const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
+                const uint32_t acc = tmem + C::ACC * (t & 1);
+#pragma unroll 1
+                for (int u = 0; u < 4; ++u) {
+                    if (!ok || !(ok = wwait(&m->ready[t & 1][u], two(t)))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 2 * u; ks < 2 * u + 2; ++ks)
+                        warp_mma_ss(leader, acc, desc_add(ad, ks * 2048), desc_add(bd, ks * 2048), C::ID2,
+                                    ks > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int ks = 2 * u; ks < 2 * u + 2; ++ks)
+                        warp_mma_ss(leader, acc + 64, desc_add(ad, ks * 2048), desc_add(bd, 2 * C::BOX + ks * 2048),
+                                    C::ID1, 1u);
+                }
+                if (ok) {
+                    warp_commit(leader, &m->empty[t & 1]);
+                    warp_commit(leader, &m->acc_full[t & 1]);
+                }
+            }
+            if (!ok) fail();
+            warp_commit(leader, &m->done);  // every issued MMA has finished before TMEM is freed
+            mbar_wait(&m->done, 0u, nullptr, tlimit);
+            __syncwarp();
         }
-        if (!ok) fail();
-        warp_commit(leader, &m->done);  // every issued MMA has finished before TMEM is freed
-        mbar_wait(&m->done, 0u, nullptr, tlimit);
-        __syncwarp();
-    } else if (warp < 6) {
+    } else if (warp < 8) {
         // ---------------------------------------------------------------- epilogue: the state
+        reg_inc<C::R_STATE>();
         const int q = warp & 3;
         // row i of the accumulators: lane i for M = 128; lanes 0..15 of each 32-lane
         // quadrant for M = 64
@@ -465,83 +520,82 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
                 X[4 * x] = f.x, X[4 * x + 1] = f.y, X[4 * x + 2] = f.z, X[4 * x + 3] = f.w;
             }
         }
-        const size_t first = (size_t)p.tab.first_block(rank);
-        // the forward snapshot's rows of this warp, fetched a block ahead: chunk lane % 8 of the
-        // eight rows that transpose_chunks hands on
-        uint4 o[8];
-        auto fetch_other = [&](int t) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                   p.other + (((first + block_of(t)) * p.H + h) * D + (i & ~7)) * D + 64 * vs) +
-                               (lane & 7);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) o[x] = i_ok ? src[x * (D / 8)] : make_uint4(0u, 0u, 0u, 0u);
-        };
-        if (REV && p.through != nullptr && nb > 0) fetch_other(0);
         float total = 0.f;
         bool ok = true;
+        // After a failed wait a warp goes on through the blocks without doing anything but meeting
+        // the others at the named barriers, so that none waits there for ever.
         for (int t = 0; t < nb; ++t) {
-            const int blk = block_of(t);
-            const size_t at = (first + blk) * p.H + h;
             // gates_ready of t + 2 needs this warp's gates_free of t
-            if (!wwait(&m->gates_ready[t & 1], (uint32_t)((t >> 1) & 1))) {
-                ok = false;
-                break;
-            }
+            if (ok) ok = wwait(&m->gates_ready[t & 1], two(t)) && (!through || wwait(&m->other_full[t & 1], two(t)));
             const float G = m->sum[t & 1], decay = exp2f(G);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
-            total += G;
-            if (REV && p.through != nullptr) {
+            if (ok) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
+                total += G;
+            }
+            if (ok && through) {
                 // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
-                transpose_chunks(o);
+                const uint32_t at = sbase + C::OFF_OTHER + (t & 1) * C::SBOX + i * 128;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
+                if (i_ok) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t in[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
+                    for (int x = 0; x < 8; ++x) {
+                        const uint4 o = ld_shared_v4(at + ((x ^ (i & 7)) << 4));
+                        const uint32_t in[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
-                        part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
+                        for (int e = 0; e < 4; ++e) {
+                            part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
+                            part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
+                        }
                     }
                 }
-                float f = i_ok ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
-                if (t + 1 < nb) fetch_other(t + 1);
+                mbar_arrive(&m->other_free[t & 1]);
+                float f = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
-                if (lane == 0) p.through[at * (4 * C::NVS) + 4 * vs + q] = decay * f;
+                if (lane == 0) p.through[(size_t)number_of(t) * (4 * C::NVS) + 4 * vs + q] = decay * f;
             }
-            if (p.snap != nullptr) {
-                uint4 c[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) c[x] = pack_chunk(&X[8 * x]);
-                transpose_chunks(c);
+            if (p.have_snap) {
+                // bf16 rows into one of two buffers, whose store of two blocks ago has read it; then
+                // one thread stores the slice
+                if (warp == 4 && lane == 0) bulk_wait_read_but_one();
+                __syncwarp();
+                named_barrier(1, C::GROUP);
+                const uint32_t at = sbase + C::OFF_SNAP + (t & 1) * C::SBOX;
                 if (i_ok) {
-                    uint4 *d = reinterpret_cast<uint4 *>(p.snap + (at * D + (i & ~7)) * D + 64 * vs) + (lane & 7);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) d[x * (D / 8)] = c[x];
+                    for (int x = 0; x < 8; ++x)
+                        st_shared_u4(at + i * 128 + ((x ^ (i & 7)) << 4), pack_chunk(&X[8 * x]));
                 }
-            }
-            if (!wwait(&m->acc_full[t & 1], (uint32_t)((t >> 1) & 1))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t tA = tmem + C::ACC * (t & 1) + lane_base;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t a[16], c[16];
-                tmem_ld16(tA + 16 * x, a);
-                tmem_ld16(tA + 64 + 16 * x, c);
-                tmem_ld_wait();
-                if (x == 3) {
-                    tc_fence_before();
-                    mbar_arrive(&m->acc_free[t & 1]);
+                fence_proxy_async_smem();
+                named_barrier(1, C::GROUP);
+                if (ok && warp == 4 && lane == 0) {
+                    tma_store_2d(&p.tmap_snap, at, 64 * vs, number_of(t) * D);
+                    bulk_commit_group();
                 }
+                __syncwarp();
+            }
+            if (ok) ok = wwait(&m->acc_full[t & 1], two(t));
+            if (ok) {
+                tc_fence_after();
+                const uint32_t tA = tmem + C::ACC * (t & 1) + lane_base;
 #pragma unroll
-                for (int z = 0; z < 16; ++z)
-                    X[16 * x + z] = fmaf(decay, X[16 * x + z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t a[32], c[32];
+                    tmem_ld32(tA + 32 * x, a);
+                    tmem_ld32(tA + 64 + 32 * x, c);
+                    tmem_ld_wait();
+                    if (x == 1) {
+                        tc_fence_before();
+                        mbar_arrive(&m->acc_free[t & 1]);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 32; ++z)
+                        X[32 * x + z] = fmaf(decay, X[32 * x + z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
+                }
             }
         }
+        if (warp == 4 && lane == 0) bulk_wait_all();
         float *to = nullptr;
         if (p.seg_out != nullptr)
             to = p.seg_out + ((size_t)sg * p.H + h) * D * D;
@@ -552,17 +606,18 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < 16; ++x) d4[x] = make_float4(X[4 * x], X[4 * x + 1], X[4 * x + 2], X[4 * x + 3]);
         }
-        if (ok && p.seg_out != nullptr && vs == 0 && q == 0 && lane == 0) p.seg_total[(size_t)sg * p.H + h] = total * 0.6931471805599453f;
+        if (ok && p.seg_out != nullptr && vs == 0 && q == 0 && lane == 0)
+            p.seg_total[(size_t)sg * p.H + h] = total * 0.6931471805599453f;
         if (!ok) fail();
     } else {
-        // ---------------------------------------------------------------- scaling warps
-        const int w8 = warp - 6;
+        // ---------------------------------------------------------------- scaling: 16 rows a warp
+        reg_dec<C::R_SCALE>();
+        const int w8 = warp - 8, u = w8 >> 1;
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
-            const int nv = rows_of(block_of(t));
+            const int nv = rows_of(t);
             const float *sg2 = reinterpret_cast<const float *>(smem + C::OFF_G) + C::C * (t & 1);
-            if (!wwait(&m->gates_ready[t & 1], (uint32_t)((t >> 1) & 1)) ||
-                !wwait(&m->full[t & 1], (uint32_t)((t >> 1) & 1))) {
+            if (!wwait(&m->gates_ready[t & 1], two(t)) || !wwait(&m->full[t & 1], two(t))) {
                 ok = false;
                 break;
             }
@@ -570,19 +625,18 @@ __global__ void __launch_bounds__(GatedStateCfg<D>::THREADS, 1)
             // chunk c of row r lies in one of the row's eight 16-byte places, whichever the
             // swizzle says; all eight are scaled alike
 #pragma unroll 2
-            for (int c = w8 * 32 + lane; c < C::C * 8; c += 32 * C::SCALERS) {
-                const int r = c >> 3;
+            for (int x = 0; x < 4; ++x) {
+                const int c = w8 * 128 + x * 32 + lane, r = c >> 3;
                 uint4 part[3];
                 split_chunk(ld_shared_v4(b + c * 16), exp2f(sg2[r]), r < nv, part);
 #pragma unroll
                 for (int y = 0; y < 3; ++y) st_shared_u4(b + y * C::BOX + c * 16, part[y]);
             }
-            if (nv < C::C)  // rows of another sequence: 0 times what they hold could be a NaN
-                for (int d = 0; d < C::DB; ++d)
-                    for (int c = nv * 8 + w8 * 32 + lane; c < C::C * 8; c += 32 * C::SCALERS)
-                        st_shared_v4(stage(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
+            // rows of another sequence: 0 times what they hold could be a NaN
+            for (int c = max(nv, 16 * w8) * 8 + lane; c < (16 * w8 + 16) * 8; c += 32)
+                for (int d = 0; d < C::DB; ++d) st_shared_v4(stage(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
-            mbar_arrive(&m->ready[t & 1]);
+            mbar_arrive(&m->ready[t & 1][u]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
         }

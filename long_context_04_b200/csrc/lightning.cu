@@ -308,10 +308,20 @@ la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, co
 }
 
 // The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
+// The kernels whose warpgroups trade registers (setmaxnreg) have to start with what the shares
+// add up to, or a group would wait for registers that nobody gives back.
+template <typename K>
+bool starts_with(K kern, int registers) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs >= registers;
+}
+
 template <int D, bool REV>
 la_status launch_gated_states(const la::GatedStateParams &p, cudaStream_t stream) {
-    using C = la::GatedStateCfg<D>;
+    using C = la::GatedStateCfg<D, REV>;
     auto kern = la::gated_state_tc_kernel<D, REV>;
+    static const bool fits = starts_with(kern, C::R_LAUNCH);
+    if (!fits) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
     kern<<<(unsigned)(p.tab.segs * p.H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
@@ -326,8 +336,7 @@ bool fill_gated_states(la::GatedStateParams &p, const void *a, const void *b, co
     p.H = H;
     p.timeout_ns = kWaitLimitNs;
     p.tab = pl.tab;
-    return make_map(&p.tmap_a, a, T, H, D, la::GatedStateCfg<D>::C) &&
-           make_map(&p.tmap_b, b, T, H, D, la::GatedStateCfg<D>::C);
+    return make_map(&p.tmap_a, a, T, H, D, 128) && make_map(&p.tmap_b, b, T, H, D, 128);
 }
 
 // The start states of a segmented call's segments (in place of their own end states).
@@ -347,9 +356,12 @@ template <int D, bool REV>
 la_status gated_states_tc(const void *a, const void *b, const void *g, const float *initial, void *snap,
                           const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
                           uint8_t *ws, cudaStream_t stream) {
-    using bf = __nv_bfloat16;
     la::GatedStateParams p;
-    if (!fill_gated_states<D>(p, a, b, g, H, T, pl)) return LA_ERR_CUDA;
+    const long long rows = (long long)pl.tab.blocks * H * D;
+    if (!fill_gated_states<D>(p, a, b, g, H, T, pl) ||
+        (snap != nullptr && !make_map(&p.tmap_snap, snap, rows, 1, D, D)) ||
+        (through != nullptr && !make_map(&p.tmap_other, other, rows, 1, D, D)))
+        return LA_ERR_CUDA;
     if (pl.segmented) {
         float *seg_in = nullptr;
         if (la_status st = gated_seg_states_tc<D, REV>(p, initial, pl, ws, stream, seg_in); st != LA_OK) return st;
@@ -357,8 +369,7 @@ la_status gated_states_tc(const void *a, const void *b, const void *g, const flo
     }
     p.initial = initial;
     p.fin = fin;
-    p.snap = static_cast<bf *>(snap);
-    p.other = static_cast<const bf *>(other);
+    p.have_snap = snap != nullptr;
     p.through = through;
     return launch_gated_states<D, REV>(p, stream);
 }
@@ -381,13 +392,7 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
                            cudaStream_t stream) {
     using C = la::GatedPrefillCfg<D>;
     auto kern = la::gated_prefill_tc_kernel<D>;
-    // The warpgroups trade registers (setmaxnreg): the block has to start with what their shares
-    // add up to, or a group would wait for registers that nobody gives back.
-    static const bool fits = [&] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
-               at.numRegs >= C::R_LAUNCH;
-    }();
+    static const bool fits = starts_with(kern, C::R_LAUNCH);
     if (!fits) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
