@@ -20,7 +20,8 @@
 // token and head.
 //
 // Warpgroups (512 threads; registers are moved to the one that holds the state):
-//   0  warp 0 TMA loads and gate sums; warp 1 MMA issue
+//   0  warp 0 loads of the tiles; warp 1 MMA issue; warp 2 gate sums; warp 3 loads of the forward
+//      snapshots (reverse scan)
 //   1  epilogue: the state, its snapshots, in the reverse scan the parts of e^{G_C} <X, state>
 //   2, 3  scaling
 #pragma once
@@ -54,12 +55,12 @@ struct GatedStateCfg {
     static constexpr int DB = D / 64;               // 64-column boxes of the left tile
     static constexpr int BOX = C * 128;             // 128 rows x 128 B
     static constexpr int SBOX = D * 128;            // a slice of a state's snapshot
-    static constexpr int STAGE = (DB + 3) * BOX;    // left tile, then the slice and its two lower parts
-    static constexpr int LOADED = (DB + 1) * BOX;
-    static constexpr int NST = 2;
-    static constexpr int OFF_SNAP = NST * STAGE;    // snapshots on their way out, two
-    static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: forward snapshots, two
-    static constexpr int OFF_G = OFF_OTHER + (REV ? 2 * SBOX : 0);        // gate sums, two blocks
+    static constexpr int STAGE = (DB + 1) * BOX;    // left tile, then the slice (later its first part)
+    static constexpr int NST = 3;
+    static constexpr int OFF_PARTS = NST * STAGE;   // the slice's second and third parts
+    static constexpr int OFF_SNAP = OFF_PARTS + 2 * BOX;                  // snapshots on their way out, two
+    static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: a forward snapshot
+    static constexpr int OFF_G = OFF_OTHER + (REV ? SBOX : 0);            // gate sums, two blocks
     static constexpr int OFF_MISC = OFF_G + 2 * C * 4;
     static constexpr int SMEM_USED = 1024 + OFF_MISC + 512;
     // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
@@ -75,10 +76,10 @@ struct GatedStateCfg {
 };
 
 struct GatedStateMisc {
-    uint64_t full[2], empty[2];            // tiles landed, released
-    uint64_t ready[2][4];                  // a quarter of the slice scaled
+    uint64_t full[3], empty[3];            // tiles landed, released
+    uint64_t ready[4], parts_free[4];      // a quarter of the slice scaled, multiplied
     uint64_t acc_full[2], acc_free[2];
-    uint64_t other_full[2], other_free[2]; // reverse: the forward snapshot of a block
+    uint64_t other_full, other_free;       // reverse: the forward snapshot of a block
     uint64_t gates_ready[2], gates_free[2];
     uint64_t done;
     float sum[2];          // log-decay of a block, times log2(e)
@@ -378,14 +379,19 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
     auto number_of = [&](int t) { return (first + block_of(t)) * p.H + h; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&m->full[i], 1);
-            for (int u = 0; u < 4; ++u) mbar_init(&m->ready[i][u], 64);
             mbar_init(&m->empty[i], 1);
+        }
+        for (int u = 0; u < 4; ++u) {
+            mbar_init(&m->ready[u], 64);
+            mbar_init(&m->parts_free[u], 1);
+        }
+        mbar_init(&m->other_full, 1);
+        mbar_init(&m->other_free, C::GROUP);
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&m->acc_full[i], 1);
             mbar_init(&m->acc_free[i], C::GROUP);
-            mbar_init(&m->other_full[i], 1);
-            mbar_init(&m->other_free[i], C::GROUP);
             mbar_init(&m->gates_ready[i], 32);
             mbar_init(&m->gates_free[i], 12);  // the warps of the epilogue and of scaling
         }
@@ -410,71 +416,49 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
-    // Every ring has two slots: use t of a slot is its phase t / 2, and a slot is refilled
-    // only after its release of use t - 2, so that each wait below sees the phase it means.
+    // Parity of use t of a ring of one, two or three slots; a slot is used again only after the
+    // release of its last use, so that each wait below sees the phase it means.
+    auto one = [](int t) { return (uint32_t)(t & 1); };
     auto two = [](int t) { return (uint32_t)((t >> 1) & 1); };
-    auto stage = [&](int t) { return sbase + (uint32_t)((t & 1) * C::STAGE); };
+    auto three = [](int t) { return (uint32_t)((t / 3) & 1); };
+    auto stage = [&](int t) { return sbase + (uint32_t)((t % 3) * C::STAGE); };
 
     if (warp < 4) {
         reg_dec<C::R_MISC>();
+        bool ok = true;
         if (warp == 0) {
-            // ------------------------------------------------------------ TMA loads, gate sums
+            // ------------------------------------------------------------ loads of the tiles
             int issued = 0;
-            uint32_t raw[4];
-            float gate[4];
-            auto fetch = [&](int t) {
-                fetch_gates4(raw, p.g, start + block_of(t) * C::C, rows_of(t), p.H, h);
-            };
-            if (nb > 0) fetch(0);
             for (int t = 0; t < nb; ++t) {
-                if (!wwait(&m->empty[t & 1], two(t) ^ 1u)) break;
+                if (!(ok = wwait(&m->empty[t % 3], three(t) ^ 1u))) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&m->full[t & 1], (uint32_t)C::LOADED);
+                    mbar_arrive_expect_tx(&m->full[t % 3], (uint32_t)C::STAGE);
                     const int row = start + block_of(t) * C::C, col = h * D;
 #pragma unroll
                     for (int d = 0; d < C::DB; ++d)
-                        tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t & 1]);
-                    tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t & 1]);
-                }
-                if (through) {
-                    if (!wwait(&m->other_free[t & 1], two(t) ^ 1u)) {
-                        // (the tiles of this block are in flight)
-                        mbar_wait(&m->full[t & 1], two(t), nullptr, tlimit);
-                        break;
-                    }
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&m->other_full[t & 1], (uint32_t)C::SBOX);
-                        tma_load_2d(sbase + C::OFF_OTHER + (t & 1) * C::SBOX, &p.tmap_other, 64 * vs,
-                                    number_of(t) * D, &m->other_full[t & 1]);
-                    }
+                        tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t % 3]);
+                    tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t % 3]);
                 }
                 ++issued;
-                if (!wwait(&m->gates_free[t & 1], two(t) ^ 1u)) break;
-                widen_gates4(gate, raw);
-                store_gate_sums<REV>(reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (t & 1), &m->sum[t & 1], gate);
-                mbar_arrive(&m->gates_ready[t & 1]);
-                if (t + 1 < nb) fetch(t + 1);
             }
-            if (issued < nb || *abort_flag) fail();
+            if (!ok) fail();
             // loads that are still in flight land before the CTA ends
-            for (int t = max(0, issued - 2); t < issued; ++t) {
-                mbar_wait(&m->full[t & 1], two(t), nullptr, tlimit);
-                if (through) mbar_wait(&m->other_full[t & 1], two(t), nullptr, tlimit);
-            }
-            __syncwarp();
+            for (int t = max(0, issued - 3); t < issued; ++t)
+                mbar_wait(&m->full[t % 3], three(t), nullptr, tlimit);
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
             const uint32_t leader = elect_leader();
-            bool ok = true;
             for (int t = 0; ok && t < nb; ++t) {
-                ok = wwait(&m->full[t & 1], two(t)) && (t < 2 || wwait(&m->acc_free[t & 1], two(t - 2)));
+                ok = wwait(&m->full[t % 3], three(t)) && (t < 2 || wwait(&m->acc_free[t & 1], two(t - 2)));
                 // [dims][2 x 64 columns] = A^T [part 0 | part 1 + part 2]
+                const uint32_t b = stage(t) + C::DB * C::BOX, parts = sbase + C::OFF_PARTS;
                 const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
-                const uint64_t bd = desc_mnmajor_sw128(stage(t) + C::DB * C::BOX, C::BOX);
+                const uint64_t bd = desc_mnmajor_sw128(b, parts - b), ld = desc_mnmajor_sw128(parts + C::BOX, C::BOX);
                 const uint32_t acc = tmem + C::ACC * (t & 1);
 #pragma unroll 1
                 for (int u = 0; u < 4; ++u) {
-                    if (!ok || !(ok = wwait(&m->ready[t & 1][u], two(t)))) break;
+                    // ready of t + 1 needs parts_free of t
+                    if (!ok || !(ok = wwait(&m->ready[u], one(t)))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 2 * u; ks < 2 * u + 2; ++ks)
@@ -482,19 +466,49 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                                     ks > 0 ? 1u : 0u);
 #pragma unroll
                     for (int ks = 2 * u; ks < 2 * u + 2; ++ks)
-                        warp_mma_ss(leader, acc + 64, desc_add(ad, ks * 2048), desc_add(bd, 2 * C::BOX + ks * 2048),
-                                    C::ID1, 1u);
+                        warp_mma_ss(leader, acc + 64, desc_add(ad, ks * 2048), desc_add(ld, ks * 2048), C::ID1, 1u);
+                    warp_commit(leader, &m->parts_free[u]);
                 }
                 if (ok) {
-                    warp_commit(leader, &m->empty[t & 1]);
+                    warp_commit(leader, &m->empty[t % 3]);
                     warp_commit(leader, &m->acc_full[t & 1]);
                 }
             }
             if (!ok) fail();
             warp_commit(leader, &m->done);  // every issued MMA has finished before TMEM is freed
             mbar_wait(&m->done, 0u, nullptr, tlimit);
-            __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ gate sums
+            uint32_t raw[4];
+            float gate[4];
+            auto fetch = [&](int t) {
+                fetch_gates4(raw, p.g, start + block_of(t) * C::C, rows_of(t), p.H, h);
+            };
+            if (nb > 0) fetch(0);
+            for (int t = 0; t < nb; ++t) {
+                if (!(ok = wwait(&m->gates_free[t & 1], two(t) ^ 1u))) break;
+                widen_gates4(gate, raw);
+                store_gate_sums<REV>(reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (t & 1), &m->sum[t & 1], gate);
+                mbar_arrive(&m->gates_ready[t & 1]);
+                if (t + 1 < nb) fetch(t + 1);
+            }
+            if (!ok) fail();
+        } else if (through) {
+            // ------------------------------------------------------------ forward snapshots
+            for (int t = 0; t < nb; ++t) {
+                if (!(ok = wwait(&m->other_free, one(t) ^ 1u))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&m->other_full, (uint32_t)C::SBOX);
+                    tma_load_2d(sbase + C::OFF_OTHER, &p.tmap_other, 64 * vs, number_of(t) * D, &m->other_full);
+                    if (t + 1 < nb) tma_prefetch_l2_2d(&p.tmap_other, 64 * vs, number_of(t + 1) * D);
+                }
+                __syncwarp();
+                // the epilogue frees the place only once this load has landed; the last one:
+                if (t == nb - 1) mbar_wait(&m->other_full, one(t), nullptr, tlimit);
+            }
+            if (!ok) fail();
         }
+        __syncwarp();
     } else if (warp < 8) {
         // ---------------------------------------------------------------- epilogue: the state
         reg_inc<C::R_STATE>();
@@ -520,13 +534,24 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 X[4 * x] = f.x, X[4 * x + 1] = f.y, X[4 * x + 2] = f.z, X[4 * x + 3] = f.w;
             }
         }
+        // reverse: this row of the block's forward snapshot, read a block ahead, so that the one
+        // place for it is refilled meanwhile
+        uint4 o[8];
+        auto take_other = [&](int t) -> bool {
+            if (!wwait(&m->other_full, one(t))) return false;
+            const uint32_t at = sbase + C::OFF_OTHER + (i_ok ? i : 0) * 128;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = ld_shared_v4(at + ((x ^ (i & 7)) << 4));
+            mbar_arrive(&m->other_free);
+            return true;
+        };
         float total = 0.f;
-        bool ok = true;
+        bool ok = !through || nb == 0 || take_other(0);
         // After a failed wait a warp goes on through the blocks without doing anything but meeting
         // the others at the named barriers, so that none waits there for ever.
         for (int t = 0; t < nb; ++t) {
             // gates_ready of t + 2 needs this warp's gates_free of t
-            if (ok) ok = wwait(&m->gates_ready[t & 1], two(t)) && (!through || wwait(&m->other_full[t & 1], two(t)));
+            if (ok) ok = wwait(&m->gates_ready[t & 1], two(t));
             const float G = m->sum[t & 1], decay = exp2f(G);
             if (ok) {
                 __syncwarp();
@@ -535,22 +560,17 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             }
             if (ok && through) {
                 // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
-                const uint32_t at = sbase + C::OFF_OTHER + (t & 1) * C::SBOX + i * 128;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
-                if (i_ok) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 o = ld_shared_v4(at + ((x ^ (i & 7)) << 4));
-                        const uint32_t in[4] = {o.x, o.y, o.z, o.w};
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t in[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
-                            part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
+                        part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
                     }
                 }
-                mbar_arrive(&m->other_free[t & 1]);
-                float f = (part[0] + part[1]) + (part[2] + part[3]);
+                float f = i_ok ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
                 if (lane == 0) p.through[(size_t)number_of(t) * (4 * C::NVS) + 4 * vs + q] = decay * f;
@@ -594,6 +614,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                         X[32 * x + z] = fmaf(decay, X[32 * x + z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
                 }
             }
+            if (ok && through && t + 1 < nb) ok = take_other(t + 1);
         }
         if (warp == 4 && lane == 0) bulk_wait_all();
         float *to = nullptr;
@@ -617,11 +638,13 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
         for (int t = 0; t < nb; ++t) {
             const int nv = rows_of(t);
             const float *sg2 = reinterpret_cast<const float *>(smem + C::OFF_G) + C::C * (t & 1);
-            if (!wwait(&m->gates_ready[t & 1], two(t)) || !wwait(&m->full[t & 1], two(t))) {
+            // parts_free of t needs ready of t
+            if (!wwait(&m->gates_ready[t & 1], two(t)) || !wwait(&m->full[t % 3], three(t)) ||
+                (t >= 1 && !wwait(&m->parts_free[u], one(t - 1)))) {
                 ok = false;
                 break;
             }
-            const uint32_t b = stage(t) + C::DB * C::BOX;
+            const uint32_t b = stage(t) + C::DB * C::BOX, parts = sbase + C::OFF_PARTS;
             // chunk c of row r lies in one of the row's eight 16-byte places, whichever the
             // swizzle says; all eight are scaled alike
 #pragma unroll 2
@@ -629,14 +652,15 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 const int c = w8 * 128 + x * 32 + lane, r = c >> 3;
                 uint4 part[3];
                 split_chunk(ld_shared_v4(b + c * 16), exp2f(sg2[r]), r < nv, part);
-#pragma unroll
-                for (int y = 0; y < 3; ++y) st_shared_u4(b + y * C::BOX + c * 16, part[y]);
+                st_shared_u4(b + c * 16, part[0]);
+                st_shared_u4(parts + c * 16, part[1]);
+                st_shared_u4(parts + C::BOX + c * 16, part[2]);
             }
             // rows of another sequence: 0 times what they hold could be a NaN
             for (int c = max(nv, 16 * w8) * 8 + lane; c < (16 * w8 + 16) * 8; c += 32)
                 for (int d = 0; d < C::DB; ++d) st_shared_v4(stage(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
-            mbar_arrive(&m->ready[t & 1][u]);
+            mbar_arrive(&m->ready[u]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
         }
