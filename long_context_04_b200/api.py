@@ -64,12 +64,12 @@ def lib() -> ctypes.CDLL:
     L.la_state_prefix.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp]
     L.la_state_prefix.restype = i32
     u64 = ctypes.c_ulonglong
-    L.la_gated_workspace.argtypes = [i32, i32, i32, i32, ip, i32, u32, i32, ctypes.POINTER(u64)]
+    L.la_gated_workspace.argtypes = [i32, i32, i32, i32, vp, i32, u32, i32, ctypes.POINTER(u64)]
     L.la_gated_workspace.restype = i32
-    L.la_gated_prefill.argtypes = [vp] * 5 + [i32] * 4 + [ip, i32, u32, vp, vp, vp, u64, vp]
+    L.la_gated_prefill.argtypes = [vp] * 5 + [i32] * 4 + [vp, i32, u32, vp, vp, vp, u64, vp]
     L.la_gated_prefill.restype = i32
     L.la_gated_prefill_backward.argtypes = ([vp] * 9 + [i32] * 4 +
-                                            [ip, i32, u32, vp, vp, vp, vp, u64, vp])
+                                            [vp, i32, u32, vp, vp, vp, vp, u64, vp])
     L.la_gated_prefill_backward.restype = i32
     L.la_gated_decode_step.argtypes = [vp] * 6 + [i32] * 3 + [vp, i32, u32, vp]
     L.la_gated_decode_step.restype = i32
@@ -351,33 +351,60 @@ def state_prefix(gathered, rank: int, *, out=None, stream=None):
     return out
 
 
+def _is(t, name, dtype, dev):
+    """``_need`` with the usual case first: at one token a call's checks cost as much as its kernel."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.device == dev and t.is_contiguous()):
+        _need(t, name, dtype, dev)
+
+
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev, stream):
+    """The stream's handle: ``_stream_ptr`` without building a Stream object where torch can."""
+    if stream is None and dev.type == "cuda" and _RAW_STREAM is not None:
+        return _RAW_STREAM(dev.index) or None
+    return _stream_ptr(stream)
+
+
+def _device_for(dev, stream):
+    """The context in which to call the library: ``_on_device`` where ``dev`` is not current already."""
+    if stream is None and dev.type == "cuda" and torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return _on_device(dev, stream)
+
+
 def _gated_shape(q, k, v, g, cu_seqlens):
-    """Checks the sequence operators share; (B, H, N, D, S, boundaries or None)."""
+    """Checks the sequence operators share; (B, H, N, D, S) and the boundaries as a host
+    array, its address and its number of sequences."""
     _need(q, "q")
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, q.dtype, q.device)
-        if t.shape != q.shape:
-            raise ValueError("q, k, v must have one shape")
-    if q.dim() == 4:
-        B, N, H, D = q.shape
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    _is(k, "k", dtype, dev)
+    _is(v, "v", dtype, dev)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("q, k, v must have one shape")
+    if len(shape) == 4:
+        B, N, H, D = shape
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens needs packed [T, H, D] inputs")
         S = B
-    elif q.dim() == 3:
-        N, H, D = q.shape
+    elif len(shape) == 3:
+        N, H, D = shape
         B, S = 1, 1 if cu_seqlens is None else len(cu_seqlens) - 1
     else:
         raise ValueError("q must be [B, N, H, D] or [T, H, D]")
     if g is not None:
-        _need(g, "g", q.dtype, q.device)
-        _need_shape(g, "g", q.shape[:-1])
-    cu = None if cu_seqlens is None else np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
-    return B, H, N, D, S, cu
+        _is(g, "g", dtype, dev)
+        _need_shape(g, "g", shape[:-1])
+    if cu_seqlens is None:
+        return (B, H, N, D, S), (None, None, 0)
+    cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    return (B, H, N, D, S), (cu, cu.ctypes.data, len(cu) - 1)
 
 
 def _need_state(t, name, shape, dev):
     if t is not None:
-        _need(t, name, torch.float32, dev)
+        _is(t, name, torch.float32, dev)
         _need_shape(t, name, shape)
 
 
@@ -412,32 +439,33 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
     ``return_state`` or ``state_out`` (final states ``[S, H, D, D]`` fp32).
     ``initial_state`` as in ``prefill``: ``state_out`` may be that tensor (update in place).
     """
-    B, H, N, D, S, cu = _gated_shape(q, k, v, g, cu_seqlens)
+    (B, H, N, D, S), (cu, cu_ptr, num_seqs) = _gated_shape(q, k, v, g, cu_seqlens)
     dev, flags = q.device, _flags_for(q.dtype)
     made = []
     if out is None:
         out = torch.empty_like(q)
         made.append(out)
-    _need(out, "out", q.dtype, dev)
-    _need_shape(out, "out", q.shape)
-    if any(_overlap(out, t) for t in (q, k, v, g) if t is not None):
-        raise ValueError("out must not overlap an input")
+    else:
+        _need(out, "out", q.dtype, dev)
+        _need_shape(out, "out", q.shape)
+        if any(_overlap(out, t) for t in (q, k, v, g) if t is not None):
+            raise ValueError("out must not overlap an input")
     st = state_out
     if return_state and st is None:
         st = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
         made.append(st)
-    _need_state(st, "state_out", (S, H, D, D), dev)
+    _need_state(state_out, "state_out", (S, H, D, D), dev)
     _need_state(initial_state, "initial_state", (S, H, D, D), dev)
-    if st is not None and initial_state is not None and st.data_ptr() != initial_state.data_ptr() \
-            and _overlap(st, initial_state):
-        raise ValueError("state_out and initial_state overlap without coinciding")
-    cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
-    n_cu = 0 if cu is None else len(cu) - 1
-    with _on_device(dev, stream):
-        ws, size = _gated_workspace((B, H, N, D), cu_ptr, n_cu, flags, 0, dev, stream)
-        rc = lib().la_gated_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr, n_cu,
+    if state_out is not None:
+        if initial_state is not None and st.data_ptr() != initial_state.data_ptr() and _overlap(st, initial_state):
+            raise ValueError("state_out and initial_state overlap without coinciding")
+        if any(_overlap(st, t) for t in (q, k, v, g, out) if t is not None):
+            raise ValueError("state_out must not overlap an input or out")
+    with _device_for(dev, stream):
+        ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 0, dev, stream)
+        rc = lib().la_gated_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr, num_seqs,
                                     flags, _ptr(initial_state), _ptr(st), _ptr(ws), size,
-                                    _stream_ptr(stream))
+                                    _stream_of(dev, stream))
         _check("la_gated_prefill", rc)
         _used_on(stream, *made)
     return (out, st) if st is not None else out
@@ -452,23 +480,21 @@ def gated_prefill_backward(q, k, v, g, do, *, cu_seqlens=None, initial_state=Non
     where ``g`` is; these are then the gradients of ``prefill`` (without ``rmsnorm``).  The
     states are recomputed: nothing has to be kept from the forward call.
     """
-    B, H, N, D, S, cu = _gated_shape(q, k, v, g, cu_seqlens)
+    (B, H, N, D, S), (cu, cu_ptr, num_seqs) = _gated_shape(q, k, v, g, cu_seqlens)
     dev, flags = q.device, _flags_for(q.dtype)
-    _need(do, "do", q.dtype, dev)
+    _is(do, "do", q.dtype, dev)
     _need_shape(do, "do", q.shape)
     _need_state(initial_state, "initial_state", (S, H, D, D), dev)
     _need_state(d_state, "d_state", (S, H, D, D), dev)
     dq, dk, dv = (torch.empty_like(q) for _ in range(3))
     dg = None if g is None else torch.empty_like(g)
     d_init = None if initial_state is None else torch.empty_like(initial_state)
-    cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
-    n_cu = 0 if cu is None else len(cu) - 1
-    with _on_device(dev, stream):
-        ws, size = _gated_workspace((B, H, N, D), cu_ptr, n_cu, flags, 1, dev, stream)
+    with _device_for(dev, stream):
+        ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 1, dev, stream)
         rc = lib().la_gated_prefill_backward(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), B, H, N, D,
-            cu_ptr, n_cu, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init), _ptr(ws), size,
-            _stream_ptr(stream))
+            cu_ptr, num_seqs, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init), _ptr(ws), size,
+            _stream_of(dev, stream))
         _check("la_gated_prefill_backward", rc)
         _used_on(stream, dq, dk, dv, dg, d_init)
     return (dq, dk, dv, dg) if d_init is None else (dq, dk, dv, dg, d_init)
@@ -484,37 +510,39 @@ def gated_decode_step(q, k, v, g, state, *, slots=None, out=None, stream=None):
     skipped too, and ``device_status`` reports it.
     """
     _need(q, "q")
-    dev = q.device
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, q.dtype, dev)
-        if t.shape != q.shape:
-            raise ValueError("q, k, v must have one shape")
-    if q.dim() != 3:
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    _is(k, "k", dtype, dev)
+    _is(v, "v", dtype, dev)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("q, k, v must have one shape")
+    if len(shape) != 3:
         raise ValueError("q must be [B, H, D]")
-    B, H, D = q.shape
+    B, H, D = shape
     if g is not None:
-        _need(g, "g", q.dtype, dev)
+        _is(g, "g", dtype, dev)
         _need_shape(g, "g", (B, H))
-    _need(state, "state", torch.float32, dev)
+    _is(state, "state", torch.float32, dev)
     if state.dim() != 4 or tuple(state.shape[1:]) != (H, D, D):
         raise ValueError("state must be [num_slots, H, D, D]")
+    num_slots = state.shape[0]
     if slots is None:
-        if state.shape[0] != B:
+        if num_slots != B:
             raise ValueError("state must be [B, H, D, D] without slots")
     else:
-        _need(slots, "slots", torch.int32, dev)
+        _is(slots, "slots", torch.int32, dev)
         _need_shape(slots, "slots", (B,))
-    flags = _flags_for(q.dtype)
+    flags = _flags_for(dtype)
     made = out is None
     if made:
         out = torch.empty_like(q)
-    _need(out, "out", q.dtype, dev)
-    _need_shape(out, "out", q.shape)
-    if any(_overlap(out, t) for t in (q, k, v, g, state) if t is not None):
-        raise ValueError("out must not overlap an input or the state")
-    with _on_device(dev, stream):
+    else:
+        _need(out, "out", dtype, dev)
+        _need_shape(out, "out", shape)
+        if any(_overlap(out, t) for t in (q, k, v, g, state) if t is not None):
+            raise ValueError("out must not overlap an input or the state")
+    with _device_for(dev, stream):
         rc = lib().la_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), B, H, D,
-                                        _ptr(slots), state.shape[0], flags, _stream_ptr(stream))
+                                        _ptr(slots), num_slots, flags, _stream_of(dev, stream))
         _check("la_gated_decode_step", rc)
         if made:
             _used_on(stream, out)
