@@ -106,17 +106,29 @@ __global__ void __launch_bounds__(256)
     tab.seqs.get(rank, start, len, sid);
     const int s0 = tab.first_seg(rank), ns = tab.num_segs(rank);
     float4 X = initial != nullptr ? initial[((size_t)sid * H + h) * n4 + x] : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int t = 0; t < ns; ++t) {
-        const size_t at = (size_t)(s0 + (rev ? ns - 1 - t : t)) * H + h;
-        const float4 l = seg_state[at * n4 + x];
-        const float a = expf(seg_total[at]);
-        seg_state[at * n4 + x] = X;
-        X = make_float4(fmaf(a, X.x, l.x), fmaf(a, X.y, l.y), fmaf(a, X.z, l.z), fmaf(a, X.w, l.w));
+    constexpr int N = 8;  // segments in flight: their loads do not wait for one another
+    for (int t0 = 0; t0 < ns; t0 += N) {
+        float4 l[N];
+        float a[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int t = t0 + e;
+            const size_t at = (size_t)(s0 + (rev ? ns - 1 - t : t)) * H + h;
+            if (t < ns) l[e] = seg_state[at * n4 + x], a[e] = seg_total[at];
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int t = t0 + e;
+            if (t >= ns) break;
+            const float w = expf(a[e]);
+            seg_state[((size_t)(s0 + (rev ? ns - 1 - t : t)) * H + h) * n4 + x] = X;
+            X = make_float4(fmaf(w, X.x, l[e].x), fmaf(w, X.y, l[e].y), fmaf(w, X.z, l[e].z), fmaf(w, X.w, l[e].w));
+        }
     }
 }
 
-// ------------------------------------------------------------------ CUDA-core kernels
-// Blocks of 64 tokens, 256 threads, tiles staged in shared memory as fp32.
+// ------------------------------------------------------------------ CUDA-core kernels (fp32)
+// Blocks of 64 tokens, 256 threads, tiles staged in shared memory.
 struct GatedSimt {
     static constexpr int C = 64;
     static constexpr int THREADS = 256;
@@ -126,15 +138,14 @@ struct GatedSimt {
 // Sums of the block's log-decays: sG[i] = g_0 + .. + g_i (i < nv; rows behind the sequence
 // repeat the last sum), in fp64, so that differences of two large sums stay exact to fp32.
 // Called by warp 0.
-template <typename T>
-__device__ __forceinline__ void simt_gate_sums(double *sG, const T *__restrict__ g, int row0, int nv,
+__device__ __forceinline__ void simt_gate_sums(double *sG, const float *__restrict__ g, int row0, int nv,
                                                int H, int h) {
     const int lane = threadIdx.x & 31;
     double carry = 0.0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = 32 * half + lane;
-        double x = i < nv && g != nullptr ? (double)clamp_gate(to_f32(g[(size_t)(row0 + i) * H + h])) : 0.0;
+        double x = i < nv && g != nullptr ? (double)clamp_gate(g[(size_t)(row0 + i) * H + h]) : 0.0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, x, off);
@@ -146,32 +157,75 @@ __device__ __forceinline__ void simt_gate_sums(double *sG, const T *__restrict__
     }
 }
 
+__device__ __forceinline__ void cp_async16(float *dst, const float *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The state scan: one CTA per (segment, head, VS state columns).
 //   forward (REV = false): X = state,           X <- e^{G_C} X + sum_j e^{G_C - G_j} k_j v_j^T
 //   reverse (REV = true):  X = state gradient,  X <- e^{G_C} X + sum_i e^{G_i} q_i do_i^T
 // (a, b) = (k, v) or (q, do).  The state before each update goes to snap[block][h]; a
 // segment starts from seg_in (segmented call) or the sequence's initial state; seg_out and
 // seg_total take a segment's own end state and decay; fin the sequence's final state.
-template <int D, typename T, bool REV>
+// The next block's tiles come by cp.async while this one is added up: a block of few heads is
+// all latency (64 x 64 x 32 products a CTA).
+template <int D>
+struct GatedStateSimt {
+    static constexpr int A = GatedSimt::C * D, B = GatedSimt::C * GatedSimt::VS;
+    static constexpr int SMEM_BYTES = 2 * (A + B) * 4;
+};
+
+template <int D, bool REV>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
-    gated_state_simt_kernel(const T *__restrict__ a, const T *__restrict__ b, const T *__restrict__ g,
+    gated_state_simt_kernel(const float *__restrict__ a, const float *__restrict__ b, const float *__restrict__ g,
                             const float *initial, const float *__restrict__ seg_in,
                             float *__restrict__ seg_out, float *__restrict__ seg_total,
                             float *__restrict__ snap, float *fin, int H,
                             const __grid_constant__ GatedTable tab) {
     constexpr int C = GatedSimt::C, VS = GatedSimt::VS, NS = D / VS, R = D / 32;
-    __shared__ __align__(16) float sA[C][D];
-    __shared__ __align__(16) float sB[C][VS];
-    __shared__ double sG[C];
+    extern __shared__ __align__(16) float simt_sm[];
+    __shared__ double sG[2][C];
     const int tid = threadIdx.x;
     const int vs = blockIdx.x % NS, h = (blockIdx.x / NS) % H, sg = blockIdx.x / (NS * H);
     int rank, s, start, len, sid;
     tab.seg(sg, rank, s);
     tab.seqs.get(rank, start, len, sid);
     const int nb = (len + C - 1) / C, ns = tab.num_segs(rank);
-    const int b0 = s * tab.seg_blocks, b1 = min(nb, b0 + tab.seg_blocks);
+    const int b0 = s * tab.seg_blocks, n = max(0, min(nb, b0 + tab.seg_blocks) - b0);
     const int x0 = (tid >> 3) * R, y0 = (tid & 7) * 4;  // this thread's rows and columns
+    auto tile_a = [&](int t) { return simt_sm + (t & 1) * GatedStateSimt<D>::A; };
+    auto tile_b = [&](int t) { return simt_sm + 2 * GatedStateSimt<D>::A + (t & 1) * GatedStateSimt<D>::B; };
+    auto block_of = [&](int t) { return REV ? b0 + n - 1 - t : b0 + t; };
+    auto load = [&](int t) {
+        const int row0 = start + block_of(t) * C, nv = min(C, len - block_of(t) * C);
+        float *sa = tile_a(t), *sb = tile_b(t);
+#pragma unroll
+        for (int i = tid; i < C * D / 4; i += GatedSimt::THREADS) {
+            const int rr = i / (D / 4), d = 4 * (i % (D / 4));
+            cp_async16(sa + rr * D + d, a + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + d, rr < nv);
+        }
+#pragma unroll
+        for (int i = tid; i < C * VS / 4; i += GatedSimt::THREADS) {
+            const int rr = i / (VS / 4), d = 4 * (i % (VS / 4));
+            cp_async16(sb + rr * VS + d, b + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + vs * VS + d, rr < nv);
+        }
+        cp_async_commit();
+    };
+    auto sums = [&](int t) {  // warp 0
+        const int blk = block_of(t);
+        simt_gate_sums(sG[t & 1], g, start + blk * C, min(C, len - blk * C), H, h);
+    };
 
+    if (n > 0) {
+        load(0);
+        if (tid < 32) sums(0);
+    }
     float4 X[R];
     const float *from = nullptr;
     if (seg_in != nullptr)
@@ -184,30 +238,35 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
                    ? *reinterpret_cast<const float4 *>(from + (size_t)(x0 + r) * D + vs * VS + y0)
                    : make_float4(0.f, 0.f, 0.f, 0.f);
     double total = 0.0;
-    for (int t = 0; t < b1 - b0; ++t) {
-        const int blk = REV ? b1 - 1 - t : b0 + t;
-        const int row0 = start + blk * C, nv = min(C, len - blk * C);
+    for (int t = 0; t < n; ++t) {
+        const int blk = block_of(t);
+        if (t + 1 < n) {
+            load(t + 1);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
         __syncthreads();
-        if (tid < 32) simt_gate_sums(sG, g, row0, nv, H, h);
+        const double *G = sG[t & 1];
+        float *sa = tile_a(t), *sb = tile_b(t);
+#pragma unroll
+        for (int i = tid; i < C * VS / 4; i += GatedSimt::THREADS) {
+            const int rr = i / (VS / 4);
+            const float w = expf((float)(REV ? G[rr] : G[C - 1] - G[rr]));
+            float4 x = reinterpret_cast<float4 *>(sb)[i];
+            reinterpret_cast<float4 *>(sb)[i] = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
+        }
         if (snap != nullptr) {
             float *dst = snap + ((size_t)(tab.first_block(rank) + blk) * H + h) * D * D;
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 *reinterpret_cast<float4 *>(dst + (size_t)(x0 + r) * D + vs * VS + y0) = X[r];
         }
+        const double block_sum = G[C - 1];
+        total += block_sum;
         __syncthreads();
-        for (int i = tid; i < C * D; i += GatedSimt::THREADS) {
-            const int rr = i / D, d = i % D;
-            sA[rr][d] = rr < nv ? to_f32(a[((size_t)(row0 + rr) * H + h) * D + d]) : 0.f;
-        }
-        for (int i = tid; i < C * VS; i += GatedSimt::THREADS) {
-            const int rr = i / VS, d = i % VS;
-            const float w = expf((float)(REV ? sG[rr] : sG[C - 1] - sG[rr]));
-            sB[rr][d] = rr < nv ? w * to_f32(b[((size_t)(row0 + rr) * H + h) * D + vs * VS + d]) : 0.f;
-        }
-        __syncthreads();
-        total += sG[C - 1];
-        const float decay = expf((float)sG[C - 1]);
+        if (tid < 32 && t + 1 < n) sums(t + 1);
+        const float decay = expf((float)block_sum);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             X[r].x *= decay;
@@ -215,18 +274,23 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
             X[r].z *= decay;
             X[r].w *= decay;
         }
-#pragma unroll 4
-        for (int c = 0; c < nv; ++c) {
-            const float4 bb = *reinterpret_cast<const float4 *>(&sB[c][y0]);
+#pragma unroll 8
+        for (int c = 0; c < C; ++c) {
+            const float4 bb = *reinterpret_cast<const float4 *>(sb + c * VS + y0);
+            float aa[R];
+            if constexpr (R == 4)
+                *reinterpret_cast<float4 *>(aa) = *reinterpret_cast<const float4 *>(sa + c * D + x0);
+            else
+                *reinterpret_cast<float2 *>(aa) = *reinterpret_cast<const float2 *>(sa + c * D + x0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float aa = sA[c][x0 + r];
-                X[r].x = fmaf(aa, bb.x, X[r].x);
-                X[r].y = fmaf(aa, bb.y, X[r].y);
-                X[r].z = fmaf(aa, bb.z, X[r].z);
-                X[r].w = fmaf(aa, bb.w, X[r].w);
+                X[r].x = fmaf(aa[r], bb.x, X[r].x);
+                X[r].y = fmaf(aa[r], bb.y, X[r].y);
+                X[r].z = fmaf(aa[r], bb.z, X[r].z);
+                X[r].w = fmaf(aa[r], bb.w, X[r].w);
             }
         }
+        __syncthreads();  // this block's tiles may be written again
     }
     float *to = nullptr;
     if (seg_out != nullptr)
@@ -252,13 +316,15 @@ struct GatedSimtTiles {
     static constexpr int BWD_BYTES = (4 * TILE + 2 * PT + ST) * 4 + GatedSimt::C * 8 + 6 * GatedSimt::C * 4 + 64;
 };
 
-template <int D, typename T>
-__device__ __forceinline__ void simt_load_tile(float *dst, const T *__restrict__ src, int row0, int nv,
-                                               int H, int h) {
+// A tile by cp.async; rows behind the sequence are zeros.
+template <int D>
+__device__ __forceinline__ void simt_load_tile(float *dst, const float *__restrict__ src, int row0, int nv, int H,
+                                               int h) {
     constexpr int LD = GatedSimtTiles<D>::LD;
-    for (int i = threadIdx.x; i < GatedSimt::C * D; i += GatedSimt::THREADS) {
-        const int r = i / D, d = i % D;
-        dst[r * LD + d] = r < nv ? to_f32(src[((size_t)(row0 + r) * H + h) * D + d]) : 0.f;
+#pragma unroll
+    for (int i = threadIdx.x; i < GatedSimt::C * D / 4; i += GatedSimt::THREADS) {
+        const int r = i / (D / 4), d = 4 * (i % (D / 4));
+        cp_async16(dst + r * LD + d, src + ((size_t)(row0 + min(r, nv - 1)) * H + h) * D + d, r < nv);
     }
 }
 
@@ -322,47 +388,60 @@ __device__ __forceinline__ void simt_rows_by_cols(float (&acc)[4][D / 16], const
 }
 
 // acc += A M (or A M^T with TM) for the D x D state M in global memory, a slab of 32
-// contracted rows at a time through shared memory.
+// contracted rows at a time through shared memory; the next slab is in registers meanwhile.
 template <int D, bool TM>
 __device__ __forceinline__ void simt_rows_by_state(float (&acc)[4][D / 16], const float *A,
                                                    const float *__restrict__ M, float *slab) {
     constexpr int LD = GatedSimtTiles<D>::LD, SR = GatedSimtTiles<D>::SROWS;
+    constexpr int N = SR * D / 4 / GatedSimt::THREADS;
+    const int tid = threadIdx.x;
+    float4 x[N];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = tid + e * GatedSimt::THREADS;
+            // TM: lane -> row of M, so that the transposed stores of a warp are consecutive
+            x[e] = TM ? *reinterpret_cast<const float4 *>(M + (size_t)(i % D) * D + c0 + 4 * (i / D))
+                      : *reinterpret_cast<const float4 *>(M + (size_t)(c0 + i / (D / 4)) * D + 4 * (i % (D / 4)));
+        }
+    };
+    fetch(0);
     for (int c0 = 0; c0 < D; c0 += SR) {
         __syncthreads();
-        if (TM) {  // slab[c][x] = M[x][c0 + c]
-            for (int i = threadIdx.x; i < SR * D; i += GatedSimt::THREADS) {
-                const int x = i / SR, c = i % SR;
-                slab[c * LD + x] = M[(size_t)x * D + c0 + c];
-            }
-        } else {
-            for (int i = threadIdx.x; i < SR * D; i += GatedSimt::THREADS) {
-                const int c = i / D, x = i % D;
-                slab[c * LD + x] = M[(size_t)(c0 + c) * D + x];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int i = tid + e * GatedSimt::THREADS;
+            if (TM) {  // slab[c][row] = M[row][c0 + c]
+                float *to = slab + 4 * (i / D) * LD + i % D;
+                to[0] = x[e].x, to[LD] = x[e].y, to[2 * LD] = x[e].z, to[3 * LD] = x[e].w;
+            } else {
+                *reinterpret_cast<float4 *>(slab + (i / (D / 4)) * LD + 4 * (i % (D / 4))) = x[e];
             }
         }
         __syncthreads();
+        if (c0 + SR < D) fetch(c0 + SR);
         simt_rows_by_cols<D, false>(acc, A + c0, LD, slab, SR);
     }
 }
 
-template <int D, typename T>
-__device__ __forceinline__ void simt_store_rows(T *__restrict__ dst, const float (&acc)[4][D / 16], int row0,
+template <int D>
+__device__ __forceinline__ void simt_store_rows(float *__restrict__ dst, const float (&acc)[4][D / 16], int row0,
                                                 int nv, int H, int h) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (4 * ty + r < nv)
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-                dst[((size_t)(row0 + 4 * ty + r) * H + h) * D + 64 * (x / 4) + 4 * tx + (x & 3)] =
-                    from_f32<T>(acc[r][x]);
+            for (int x = 0; x < D / 64; ++x)
+                *reinterpret_cast<float4 *>(dst + ((size_t)(row0 + 4 * ty + r) * H + h) * D + 64 * x + 4 * tx) =
+                    make_float4(acc[r][4 * x], acc[r][4 * x + 1], acc[r][4 * x + 2], acc[r][4 * x + 3]);
 }
 
 // Output of one block of one head, from the state at its start (snap; nullptr: zero).
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
-    gated_prefill_simt_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                              const T *__restrict__ g, T *__restrict__ o, const float *__restrict__ snap,
+    gated_prefill_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                              const float *__restrict__ g, float *__restrict__ o, const float *__restrict__ snap,
                               int H, const __grid_constant__ GatedTable tab) {
     using L = GatedSimtTiles<D>;
     constexpr int C = GatedSimt::C;
@@ -378,7 +457,9 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     simt_load_tile<D>(sQ, q, row0, nv, H, h);
     simt_load_tile<D>(sK, k, row0, nv, H, h);
     simt_load_tile<D>(sV, v, row0, nv, H, h);
+    cp_async_commit();
     if (threadIdx.x < 32) simt_gate_sums(sG, g, row0, nv, H, h);
+    cp_async_wait<0>();
     __syncthreads();
     {
         float p[4][4] = {};
@@ -415,11 +496,11 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 
 // Gradients of one block of one head, from the state at its start (snap) and the state's
 // gradient at its end (dsnap); either may be nullptr for zero.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
-    gated_backward_simt_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                               const T *__restrict__ g, const T *__restrict__ dout, T *__restrict__ dq,
-                               T *__restrict__ dk, T *__restrict__ dv, T *__restrict__ dg,
+    gated_backward_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+                               const float *__restrict__ g, const float *__restrict__ dout, float *__restrict__ dq,
+                               float *__restrict__ dk, float *__restrict__ dv, float *__restrict__ dg,
                                const float *__restrict__ snap, const float *__restrict__ dsnap, int H,
                                const __grid_constant__ GatedTable tab) {
     using L = GatedSimtTiles<D>;
@@ -445,7 +526,9 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     simt_load_tile<D>(sK, k, row0, nv, H, h);
     simt_load_tile<D>(sV, v, row0, nv, H, h);
     simt_load_tile<D>(sO, dout, row0, nv, H, h);
+    cp_async_commit();
     if (tid < 32) simt_gate_sums(sG, g, row0, nv, H, h);
+    cp_async_wait<0>();
     __syncthreads();
     float wrow[4], wcol[4];  // e^{G_i}, e^{G_C - G_j} of this thread's rows
 #pragma unroll
@@ -561,8 +644,8 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         if (tid == 0) before = 0.f;
         float after = __shfl_down_sync(0xffffffffu, up, 1);   // sum_{i >= t0 + 2}
         if (tid == 31) after = 0.f;
-        if (t0 < nv) dg[(size_t)(row0 + t0) * H + h] = from_f32<T>(through + up + before);
-        if (t0 + 1 < nv) dg[(size_t)(row0 + t0 + 1) * H + h] = from_f32<T>(through + after + r1 + before + e0);
+        if (t0 < nv) dg[(size_t)(row0 + t0) * H + h] = through + up + before;
+        if (t0 + 1 < nv) dg[(size_t)(row0 + t0 + 1) * H + h] = through + after + r1 + before + e0;
     }
 }
 

@@ -176,9 +176,12 @@ struct GatedPlan {
 };
 
 // The table and the workspace of a call.  A state scan runs one CTA per (segment, head,
-// slice) one block after the other.  A sequence is cut into segments where the longest one
-// would take more than twice the time that the whole call needs on a full GPU: the segments'
-// own end states then come first (the inputs of the scan are read twice).
+// slice), one block after the other.  Cutting sequences into segments shortens the longest
+// chain, at the price of a scan before (the segments' own end states, a second read of the
+// scan's inputs) and a kernel that joins them.  Segments as long as fill the GPU once, at
+// least 8 blocks; taken where they pay: two scans of `seg` blocks, two more launches and the
+// joining take about the time of 20 blocks (measured: 1.2 to 1.6 us a block, 8 us a launch,
+// 8 to 12 us the joining) on top of 2 seg.
 la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs, unsigned flags,
                      bool backward, GatedPlan &pl, long long &T) {
     int S = 0;
@@ -199,9 +202,28 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         pl.longest = std::max(pl.longest, nb);
         blocks += t.seqs.varlen ? nb : (long long)nb * S;
     }
-    const long long even = (blocks * H * slices + resident - 1) / resident;
-    const long long seg = std::max<long long>(min_seg, even);
-    pl.segmented = pl.longest > 2 * seg;
+    // the shortest segments of which no more than `resident` CTAs come, else of which every CTA
+    // has about the same share
+    auto segments = [&](long long seg) {
+        if (!t.seqs.varlen) return (long long)S * std::max(1ll, (pl.longest + seg - 1) / seg);
+        long long n = 0;
+        for (int r = 0; r < S; ++r) n += std::max(1ll, ((t.seqs.seq_len[r] + C - 1) / C + seg - 1) / seg);
+        return n;
+    };
+    const long long room = resident / ((long long)H * slices);
+    long long seg = std::max<long long>(min_seg, (blocks * H * slices + resident - 1) / resident);
+    if (S <= room) {
+        long long lo = seg, hi = std::max<long long>(seg, pl.longest);  // segments(hi) <= room
+        while (lo < hi) {
+            const long long mid = (lo + hi) / 2;
+            if (segments(mid) <= room)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        seg = lo;
+    }
+    pl.segmented = pl.longest > 2 * seg + 20;
     t.seg_blocks = pl.segmented ? (int)seg : std::max(1, pl.longest);
     long long nblk = 0, nseg = 0;
     if (t.seqs.varlen) {
@@ -244,16 +266,19 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
 la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 // State scan of one direction: snapshots per block, the final state where wanted.
-template <int D, typename T, bool REV>
-la_status gated_states_simt(const T *a, const T *b, const T *g, const float *initial, float *snap, float *fin,
-                            int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
-    auto kern = la::gated_state_simt_kernel<D, T, REV>;
+template <int D, bool REV>
+la_status gated_states_simt(const float *a, const float *b, const float *g, const float *initial, float *snap,
+                            float *fin, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+    auto kern = la::gated_state_simt_kernel<D, REV>;
+    constexpr int smem = la::GatedStateSimt<D>::SMEM_BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return LA_ERR_CUDA;
     const unsigned grid = (unsigned)(pl.tab.segs * H * (D / la::GatedSimt::VS));
     float *seg_state = nullptr, *seg_total = nullptr;
     if (pl.segmented) {
         seg_state = reinterpret_cast<float *>(ws + pl.seg_state);
         seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
-        kern<<<grid, la::GatedSimt::THREADS, 0, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
+        kern<<<grid, la::GatedSimt::THREADS, smem, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
                                                          nullptr, nullptr, H, pl.tab);
         if (la_status st = launched(); st != LA_OK) return st;
         la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
@@ -261,21 +286,22 @@ la_status gated_states_simt(const T *a, const T *b, const T *g, const float *ini
             D * D / 4, REV ? 1 : 0, pl.tab);
         if (la_status st = launched(); st != LA_OK) return st;
     }
-    kern<<<grid, la::GatedSimt::THREADS, 0, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
+    kern<<<grid, la::GatedSimt::THREADS, smem, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
                                                      H, pl.tab);
     return launched();
 }
 
-template <int D, typename T>
-la_status gated_prefill_simt(const T *q, const T *k, const T *v, const T *g, T *o, const float *state_in,
-                             float *state_out, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+template <int D>
+la_status gated_prefill_simt(const float *q, const float *k, const float *v, const float *g, float *o,
+                             const float *state_in, float *state_out, int H, const GatedPlan &pl, uint8_t *ws,
+                             cudaStream_t stream) {
     float *snap = nullptr;
     if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
     if (snap != nullptr || state_out != nullptr)
-        if (la_status st = gated_states_simt<D, T, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
             st != LA_OK)
             return st;
-    auto kern = la::gated_prefill_simt_kernel<D, T>;
+    auto kern = la::gated_prefill_simt_kernel<D>;
     constexpr int smem = la::GatedSimtTiles<D>::FWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
@@ -283,22 +309,22 @@ la_status gated_prefill_simt(const T *q, const T *k, const T *v, const T *g, T *
     return launched();
 }
 
-template <int D, typename T>
-la_status gated_backward_simt(const T *q, const T *k, const T *v, const T *g, const T *dout, T *dq, T *dk, T *dv,
-                              T *dg, const float *state_in, const float *d_state, float *d_state_in, int H,
-                              const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+template <int D>
+la_status gated_backward_simt(const float *q, const float *k, const float *v, const float *g, const float *dout,
+                              float *dq, float *dk, float *dv, float *dg, const float *state_in, const float *d_state,
+                              float *d_state_in, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
     float *snap = nullptr, *dsnap = nullptr;
     if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
     if (pl.longest > 1 || d_state != nullptr) dsnap = reinterpret_cast<float *>(ws + pl.dsnap);
     if (snap != nullptr)
-        if (la_status st = gated_states_simt<D, T, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, stream);
             st != LA_OK)
             return st;
     if (dsnap != nullptr || d_state_in != nullptr)
-        if (la_status st = gated_states_simt<D, T, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, stream);
             st != LA_OK)
             return st;
-    auto kern = la::gated_backward_simt_kernel<D, T>;
+    auto kern = la::gated_backward_simt_kernel<D>;
     constexpr int smem = la::GatedSimtTiles<D>::BWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
