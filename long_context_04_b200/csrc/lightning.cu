@@ -179,20 +179,19 @@ struct GatedPlan {
 // slice), one block after the other.  Cutting sequences into segments shortens the longest
 // chain, at the price of a scan before (the segments' own end states, a second read of the
 // scan's inputs) and a kernel that joins them.  Segments as long as fill the GPU once, at
-// least 8 blocks; taken where they pay: two scans of `seg` blocks, two more launches and the
-// joining take about the time of 20 blocks (measured: 1.2 to 1.6 us a block, 8 us a launch,
-// 8 to 12 us the joining) on top of 2 seg.
+// least 4 blocks; taken where they pay: beside two scans of `seg` blocks there is a second
+// scan's start and the joining, about the time of 12 blocks (measured: 1.2 to 1.6 us a block,
+// 8 us a start, 6 us the joining).
 la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs, unsigned flags,
                      bool backward, GatedPlan &pl, long long &T) {
     int S = 0;
     GatedTable &t = pl.tab;
     if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
-    // tensor cores: 128-token blocks, one CTA per SM, bf16 snapshots (of the backward pass
-    // alone: the prefill kernel keeps its state on chip); CUDA cores: 64-token blocks, four
-    // CTAs per SM, fp32 snapshots
+    // tensor cores: 128-token blocks, bf16 snapshots (of the backward pass alone: the prefill
+    // kernel keeps its state on chip); CUDA cores: 64-token blocks, fp32 snapshots
     const bool tc = (flags & LA_BF16) != 0;
     const int C = tc ? 128 : la::GatedSimt::C, slices = tc ? D / 64 : D / la::GatedSimt::VS;
-    const int resident = tc ? kSMs : 4 * kSMs, min_seg = 8;
+    const int resident = kSMs, min_seg = 4;
     t.S = S;
     t.C = C;
     long long blocks = 0;
@@ -223,7 +222,7 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         }
         seg = lo;
     }
-    pl.segmented = pl.longest > 2 * seg + 20;
+    pl.segmented = pl.longest > 2 * seg + 12;
     t.seg_blocks = pl.segmented ? (int)seg : std::max(1, pl.longest);
     long long nblk = 0, nseg = 0;
     if (t.seqs.varlen) {
