@@ -201,7 +201,8 @@ la_status la_state_out(const float *state_ws, float *state_dst, int S, int H, in
  *
  * with one log-decay g per token and head (natural logarithm; usually <= 0).  g = 0 (or
  * g == NULL) is the ungated recurrence of la_prefill and la_decode_step.  g = -inf forgets
- * the state (values below -110 count as -110: e^-110 is 0 in fp32).
+ * the state (values below -110 count as -110: e^-110 is 0 in fp32).  g > 0 lets it grow: the
+ * sum of g over 128 tokens in a row has to stay below 88, where e^g leaves fp32.
  *
  *   g         [T][H], the dtype of q; NULL: no decay.  Element-aligned.
  *   flags     LA_BF16 or LA_FP32 alone.

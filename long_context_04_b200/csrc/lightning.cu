@@ -5,6 +5,7 @@
 // prefill_pair.cuh and prefill_tc.cuh (bf16, tcgen05), prefill_simt.cuh (fp32),
 // chunk_state.cuh, decode.cuh and the gated*.cuh files.
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -335,18 +336,22 @@ la_status gated_backward_simt(const float *q, const float *k, const float *v, co
 // The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
 // The kernels whose warpgroups trade registers (setmaxnreg) have to start with what the shares
 // add up to, or a group would wait for registers that nobody gives back.
+// The registers are a property of the build, so they are asked for until the first answer.
 template <typename K>
-bool starts_with(K kern, int registers) {
+bool starts_with(K kern, int registers, std::atomic<bool> &known) {
+    if (known.load(std::memory_order_relaxed)) return true;
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs >= registers;
+    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < registers) return false;
+    known.store(true, std::memory_order_relaxed);
+    return true;
 }
 
 template <int D, bool REV>
 la_status launch_gated_states(const la::GatedStateParams &p, cudaStream_t stream) {
     using C = la::GatedStateCfg<D, REV>;
     auto kern = la::gated_state_tc_kernel<D, REV>;
-    static const bool fits = starts_with(kern, C::R_LAUNCH);
-    if (!fits) return LA_ERR_CUDA;
+    static std::atomic<bool> fits{false};
+    if (!starts_with(kern, C::R_LAUNCH, fits)) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
     kern<<<(unsigned)(p.tab.segs * p.H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
@@ -417,8 +422,8 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
                            cudaStream_t stream) {
     using C = la::GatedPrefillCfg<D>;
     auto kern = la::gated_prefill_tc_kernel<D>;
-    static const bool fits = starts_with(kern, C::R_LAUNCH);
-    if (!fits) return LA_ERR_CUDA;
+    static std::atomic<bool> fits{false};
+    if (!starts_with(kern, C::R_LAUNCH, fits)) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
     la::GatedPrefillParams p;
@@ -520,7 +525,7 @@ const char *la_status_string(la_status s) {
     return "LA_ERR_UNKNOWN";
 }
 
-int la_version(void) { return 100; }
+int la_version(void) { return 200; }
 
 la_status la_prefill(const void *q, const void *k, const void *v, void *o, int B, int H, int N,
                      int D, int beta, const int32_t *cu_seqlens, int num_seqs, unsigned flags,

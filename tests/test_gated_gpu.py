@@ -149,6 +149,38 @@ def test_prefill_leaves_other_rows(dtype):
     assert bool((big[cu[-1]:] == 7).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_no_tokens(dtype):
+    """Sequences without tokens: states pass through, gradients too, nothing else is touched."""
+    q, g = torch.zeros(0, 2, 64, dtype=dtype, device="cuda"), torch.zeros(0, 2, dtype=dtype, device="cuda")
+    x = torch.randn(2, 2, 64, 64, device="cuda")
+    o, st = api.gated_prefill(q, q, q, g, cu_seqlens=[0, 0, 0], initial_state=x, return_state=True)
+    ok()
+    assert o.shape == q.shape and torch.equal(st, x)
+    assert not api.gated_prefill(q, q, q, g, cu_seqlens=[0, 0, 0], return_state=True)[1].any()
+    got = api.gated_prefill_backward(q, q, q, g, q, cu_seqlens=[0, 0, 0], initial_state=x, d_state=2 * x)
+    ok()
+    assert torch.equal(got[4], 2 * x) and all(t.numel() == 0 for t in got[:4])
+    assert not api.gated_prefill_backward(q, q, q, g, q, cu_seqlens=[0, 0, 0], initial_state=x)[4].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_many_short_sequences(dtype):
+    """More sequences than a packed call may name, as one uniform batch; and 1024 packed ones."""
+    H, D = 1, 64
+    x = inputs([0, 1100 * 3], H, D, dtype, 8, "cuda")
+    o = api.gated_prefill(*(x[n].view(1100, 3, H, -1) for n in "qkv"), x["g"].view(1100, 3, H))
+    ok()
+    ref, _ = gated.prefill(x["q"], x["k"], x["v"], x["g"], list(range(0, 3301, 3)))
+    assert rel(o.view(-1, H, D), ref) <= out_tol(dtype)
+    cu = [0] + [3 * i + 1 for i in range(1024)]  # the first of one token, the others of three
+    n = cu[-1]
+    p = api.gated_prefill(*(x[k][:n].contiguous() for k in "qkvg"), cu_seqlens=cu)
+    ok()
+    ref, _ = gated.prefill(*(x[k][:n] for k in "qkvg"), cu)
+    assert rel(p, ref) <= out_tol(dtype)
+
+
 # ------------------------------------------------------------------ backward
 @pytest.mark.parametrize("dtype,D", KINDS, ids=IDS)
 @pytest.mark.parametrize("lengths", LENGTHS.values(), ids=LENGTHS.keys())
@@ -169,6 +201,16 @@ def test_backward_gates(dtype, D, kind):
 def test_backward_long_and_few_heads(dtype, D):
     cu = bounds([5, 4500, 0, 130])
     check_backward(inputs(cu, 1, D, dtype, 13, "cuda", kind="mild", grad=True, states=True), cu, dtype)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS, ids=IDS)
+@pytest.mark.parametrize("which", ["initial", "d_state"])
+def test_backward_with_one_of_the_states(dtype, D, which):
+    for lengths in ([100], [200, 0, 60]):
+        cu = bounds(lengths)
+        x = inputs(cu, 2, D, dtype, 17, "cuda", grad=True, states=True)
+        del x["d_state" if which == "initial" else "initial"]
+        check_backward(x, cu, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
