@@ -18,11 +18,11 @@
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
-// Warps: 0 TMA loads and gate sums; 1 MMA issue and dg; 2-9 (group A) scores -> P, dP, W, then
-// dv and dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out.
-// Every barrier completes one phase per block, and all warps meet at the block's end; the
-// next block's tiles are fetched into L2 while this one computes and loaded while its results
-// go out.
+// Warps: 0 TMA loads and gate sums; 1 MMA issue; 2-9 (group A) scores -> P, dP, W, then dv and
+// dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out; 14 dg.
+// Every barrier completes one phase per block.  The next block's tiles are fetched into L2
+// while this one computes, loaded when its last product is done, and multiplied (s, t and the
+// first terms) while its results go out.
 //
 // HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head
 // (2304 at D = 128); tensor: 8 products of 512 cycles per block.
@@ -56,13 +56,14 @@ struct GatedBackwardCfg {
     static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
     static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
     static constexpr int OFF_DP = OFF_S;
-    static constexpr int OFF_F = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 9 arrays of 128 floats
+    static constexpr int OFF_STAGE = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 2 KB per storing warp
+    static constexpr int OFF_F = OFF_STAGE + 12 * 2048;                     // 9 arrays of 128 floats
     static constexpr int OFF_MISC = OFF_F + 9 * 512;
     static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
     static_assert(DB * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
     static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     static constexpr int TM_S = 0, TM_T = 128, TM_DQ = 256, TM_DK = 384, TM_DV1 = 0, TM_DV2 = 128;
-    static constexpr int GROUP_A = 256, GROUP_B = 128, THREADS = 64 + GROUP_A + GROUP_B;
+    static constexpr int GROUP_A = 256, GROUP_B = 128, THREADS = 96 + GROUP_A + GROUP_B;
     static constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, 0, 0);
     static constexpr uint32_t ID_KK = idesc_bf16_f32(128, D, 0, 0);
     static constexpr uint32_t ID_KN = idesc_bf16_f32(128, D, 0, 1);
@@ -76,6 +77,9 @@ struct GatedBackwardMisc {
     uint64_t s_free;                      // group A has read s and t
     uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
     uint64_t dv_full, dq_full, out_full;  // dv; dq; dk, and with it every product
+    uint64_t dv_read, dq_read, dk_read;   // their accumulators have been read
+    uint64_t dg_done;                     // the sums that dg is made of have been read
+    uint64_t tail;                        // rows behind the sequence's end zeroed (blocks that have some)
     uint64_t done;
     float sum;                            // log-decay of the block, times log2(e)
     uint32_t tmem_base;
@@ -128,6 +132,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         mbar_init(&m->p_ready, C::GROUP_A);
         mbar_init(&m->scaled, C::GROUP_B);
         mbar_init(&m->out_full, 1);
+        mbar_init(&m->dv_read, C::GROUP_A);
+        mbar_init(&m->dk_read, C::GROUP_A);
+        mbar_init(&m->dq_read, C::GROUP_B);
+        mbar_init(&m->dg_done, 32);
+        mbar_init(&m->tail, 32);
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
         fence_mbarrier_init_cluster();
@@ -209,34 +218,40 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     }
     const uint32_t leader = elect_leader();
     bool ok = true;
-    uint32_t ph = 0;
-    for (int x = blockIdx.x; x < tiles; x += gridDim.x, ph ^= 1u) {
+    // Phase of the block's barriers, of the block before, and of `tail`.  Every wait is exact: no
+    // barrier's next phase completes before all who wait for this one have returned.  Loads of
+    // the next block need out_full, hence p_ready and scaled, hence groups A's and B's waits;
+    // its products need dv_read, dq_read and dk_read; its sums (p_ready, scaled) dg_done.
+    uint32_t ph = 0, tail_ph = 0;
+    for (int x = blockIdx.x; ok && x < tiles; x += gridDim.x, ph ^= 1u) {
         const int h = x % p.H;
         int rank, blk, start, len, sid;
         p.tab.block(x / p.H, rank, blk);
         p.tab.seqs.get(rank, start, len, sid);
         const int row0 = start + blk * C::C, nv = min(C::C, len - blk * C::C);
         const int next = x + (int)gridDim.x;
-        if (nv < C::C) {
-            // rows of the next sequence must not enter any sum over the block's tokens
-            if (ok) ok = wwait(&m->full_qk, ph) && wwait(&m->full_vo, ph);
-            for (int t = 0; t < 4 * C::DB; ++t)
-                for (int c = nv * 8 + tid; c < C::C * 8; c += C::THREADS)
-                    st_shared_v4(sbase + t * C::BOX + c * 16, 0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncthreads();
-        }
+        const bool first = x == (int)blockIdx.x, tail = nv < C::C;
         if (warp == 0) {
             // ------------------------------------------------------------ gate sums, loads
             float gate[4];
             widen_gates4(gate, raw);
             store_gate_sums(sG, &m->sum, gate);
             mbar_arrive(&m->gates);
+            if (tail) {
+                // rows of the next sequence must not enter any sum over the block's tokens
+                ok = wwait(&m->full_qk, ph) && wwait(&m->full_vo, ph);
+                if (!ok) break;
+                for (int t = 0; t < 4 * C::DB; ++t)
+                    for (int c = nv * 8 + lane; c < C::C * 8; c += 32)
+                        st_shared_v4(sbase + t * C::BOX + c * 16, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                mbar_arrive(&m->tail);
+            }
             if (next < tiles) {
                 fetch(next);
                 prefetch(next);
             }
-            if (ok) ok = wwait(&m->out_full, ph);
+            ok = wwait(&m->out_full, ph);
             if (ok && next < tiles) load_tiles(next);  // every product that reads the tiles is done
             __syncwarp();
         } else if (warp == 1) {
@@ -256,7 +271,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             };
             const uint64_t qk = desc_kmajor_sw128(sbase + C::OFF_Q), kkd = desc_kmajor_sw128(sbase + C::OFF_K),
                            vk = desc_kmajor_sw128(sbase + C::OFF_V), ok_ = desc_kmajor_sw128(sbase + C::OFF_DO);
-            if (ok) ok = wwait(&m->full_qk, ph);
+            ok = wwait(&m->full_qk, ph) && (!tail || wwait(&m->tail, tail_ph)) && (first || wwait(&m->dv_read, ph ^ 1u));
             if (ok) {
                 tc_fence_after();
                 product(C::TM_S, qk, kk, kkd, kk, C::ID_S, D / 16, false);
@@ -265,19 +280,21 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             if (ok) {
                 tc_fence_after();
                 product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
-                ok = wwait(&m->full_ss, ph);
+                ok = wwait(&m->full_ss, ph) && (first || wwait(&m->dq_read, ph ^ 1u));
             }
             if (ok) {
                 tc_fence_after();
                 if (p.have_s)
                     product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
+                ok = first || wwait(&m->dk_read, ph ^ 1u);
+            }
+            if (ok) {
+                tc_fence_after();
                 if (p.have_ds)
                     product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
                 warp_commit(leader, &m->first_full);
                 ok = wwait(&m->s_free, ph);
             }
-            float part = 0.f;
-            if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
             if (ok) {
                 tc_fence_after();
                 if (p.have_ds)
@@ -301,18 +318,26 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                         desc_mnmajor_sw128(sbase + C::OFF_Q, C::BOX), nn, C::ID_NN, C::C / 16, p.have_ds != 0);
                 warp_commit(leader, &m->out_full);
             }
-            if (ok && p.dg != nullptr) {
+            __syncwarp();
+        } else if (warp == 14) {
+            // ------------------------------------------------------------ dg
+            float part = 0.f;
+            if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
+            ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
+            if (!ok) break;
+            float r[4], e[4], up[4], down[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int t = 4 * lane + y;
+                r[y] = sR[t];
+                e[y] = sE[t] + (((sCol[t] + sCol[128 + t]) + (sCol[256 + t] + sCol[384 + t])) -
+                                (sRow[t] + sRow[128 + t]));
+            }
+            mbar_arrive(&m->dg_done);
+            if (p.dg != nullptr) {
                 // dg_t = e^{G_C} <dS, S> + sum_{i >= t} sR_i + sum_{j < t} (sE_j + col_j - row_j)
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-                float r[4], e[4], up[4], down[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = 4 * lane + y;
-                    r[y] = sR[t];
-                    e[y] = sE[t] + (((sCol[t] + sCol[128 + t]) + (sCol[256 + t] + sCol[384 + t])) -
-                                    (sRow[t] + sRow[128 + t]));
-                }
                 prefix_gates4(e, down);   // down[y] = sum_{j <= t}
                 suffix_gates4(r, up);     // up[y] = sum_{i > t}
 #pragma unroll
@@ -331,41 +356,48 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             const bool A = warp < 2 + C::GROUP_A / 32;
             const int half = A ? (warp - 2) >> 2 : 0;
             // 64 columns of this warp's rows out of TMEM and into `out`; with `twice`, dv's first
-            // term times w is added.
+            // term times w is added.  32 columns at a time pass through the warp's 2 KB of shared
+            // memory (rows of 64 bytes, chunk c of row r at c ^ (r / 2 % 4)), to be stored eight rows
+            // at a time: from registers a store would touch 32 rows, 32 passes of the memory pipe.
+            const uint32_t stage = sbase + C::OFF_STAGE + (warp - 2) * 2048;
             auto store = [&](uint32_t col, bool twice, float w, __nv_bfloat16 *out, int box) {
-                uint4 c[8];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t a[16];
-                    tmem_ld16(tmem + col + 64 * box + 16 * x + lanes, a);
+#pragma unroll 1
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t a[32];
+                    tmem_ld32(tmem + col + 64 * box + 32 * cc + lanes, a);
                     if (twice) {
-                        uint32_t b[16];
-                        tmem_ld16(tmem + C::TM_DV1 + 64 * box + 16 * x + lanes, b);
+                        uint32_t b[32];
+                        tmem_ld32(tmem + C::TM_DV1 + 64 * box + 32 * cc + lanes, b);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
+                        for (int y = 0; y < 32; ++y)
                             a[y] = __float_as_uint(fmaf(w, __uint_as_float(b[y]), __uint_as_float(a[y])));
                     }
                     tmem_ld_wait();
+                    __syncwarp();  // the last pass has been read back
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        c[2 * x + y] =
-                            make_uint4(pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
-                                       pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
-                                       pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
-                                       pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                    for (int y = 0; y < 4; ++y)
+                        st_shared_v4(stage + lane * 64 + ((y ^ ((lane >> 1) & 3)) << 4),
+                                     pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
+                                     pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                    __syncwarp();
+                    const int r0 = lane >> 2, c = lane & 3;
+                    __nv_bfloat16 *dst =
+                        out + ((size_t)(row0 + 32 * q + r0) * p.H + h) * D + 64 * box + 32 * cc + 8 * c;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int r = 8 * y + r0;
+                        const uint4 v = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                        if (32 * q + r < nv) *reinterpret_cast<uint4 *>(dst + (size_t)(8 * y) * p.H * D) = v;
+                    }
                 }
-                transpose_chunks(c);
-                const int r0 = i & ~7;
-                __nv_bfloat16 *dst = out + ((size_t)(row0 + r0) * p.H + h) * D + 64 * box + 8 * (lane & 7);
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    if (r0 + x < nv) *reinterpret_cast<uint4 *>(dst + (size_t)x * p.H * D) = c[x];
             };
             if (A) {
                 // -------------------------------------------------------- group A: P, dP, W
                 // (behind first_full v and S have been read: P and dP may take their places)
-                if (ok) ok = wwait(&m->gates, ph) && wwait(&m->first_full, ph);
+                ok = wwait(&m->gates, ph) && wwait(&m->first_full, ph) && (first || wwait(&m->dg_done, ph ^ 1u));
                 float wt = 0.f;
                 if (ok) {
                     tc_fence_after();
@@ -439,18 +471,20 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 }
                 // results: dv while the products of dq and dk run, then dk
 #pragma unroll 1
-                for (int n = 0; n < 2; ++n) {
-                    if (ok && n == 1) ok = wwait(&m->out_full, ph);
+                for (int n = 0; ok && n < 2; ++n) {
+                    if (n == 1) ok = wwait(&m->out_full, ph);
                     if (!ok) break;
                     tc_fence_after();
                     if (half < C::DB)
                         store(n == 0 ? C::TM_DV2 : C::TM_DK, n == 0 && p.have_ds != 0, wt, n == 0 ? p.dv : p.dk, half);
                     tc_fence_before();
+                    mbar_arrive(n == 0 ? &m->dv_read : &m->dk_read);
                 }
             } else {
                 // -------------------------------------------------------- group B: first terms
                 float r = 0.f, e = 0.f;
-                if (ok) ok = wwait(&m->gates, ph) && wwait(&m->full_qk, ph) && wwait(&m->first_full, ph);
+                ok = wwait(&m->gates, ph) && wwait(&m->full_qk, ph) && wwait(&m->first_full, ph) &&
+                     (!tail || wwait(&m->tail, tail_ph)) && (first || wwait(&m->dg_done, ph ^ 1u));
                 if (ok) {
                     tc_fence_after();
                     // rows of accumulators times w; their product with a row of q or k
@@ -495,17 +529,13 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
 #pragma unroll 1
                     for (int n = 0; n < C::DB; ++n) store(C::TM_DQ, false, 0.f, p.dq, n);
                     tc_fence_before();
+                    mbar_arrive(&m->dq_read);
                 }
             }
         }
-        if (!ok) fail();
-        // TMEM, the decays and the sums are free for the next block
-        if (__syncthreads_or(!ok)) {
-            ok = false;
-            break;
-        }
-        tc_fence_after();
+        if (tail) tail_ph ^= 1u;
     }
+    if (!ok) fail();
     if (warp == 0 && !ok) {  // loads that are still in flight land before the CTA ends
         if (loads > 0) {
             mbar_wait(&m->full_qk, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
