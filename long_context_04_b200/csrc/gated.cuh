@@ -179,10 +179,11 @@ template <int D>
 struct GatedStateSimt {
     static constexpr int A = GatedSimt::C * D, B = GatedSimt::C * GatedSimt::VS;
     static constexpr int SMEM_BYTES = 2 * (A + B) * 4;
+    static constexpr int THREADS = GatedSimt::THREADS + 32;  // one warp forms the gate sums
 };
 
 template <int D, bool REV>
-__global__ void __launch_bounds__(GatedSimt::THREADS)
+__global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
     gated_state_simt_kernel(const float *__restrict__ a, const float *__restrict__ b, const float *__restrict__ g,
                             const float *initial, const float *__restrict__ seg_in,
                             float *__restrict__ seg_out, float *__restrict__ seg_total,
@@ -217,14 +218,17 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         }
         cp_async_commit();
     };
-    auto sums = [&](int t) {  // warp 0
+    const bool adds = tid < GatedSimt::THREADS;  // the last warp: gate sums of the next block
+    auto sums = [&](int t) {
         const int blk = block_of(t);
         simt_gate_sums(sG[t & 1], g, start + blk * C, min(C, len - blk * C), H, h);
     };
 
     if (n > 0) {
-        load(0);
-        if (tid < 32) sums(0);
+        if (adds)
+            load(0);
+        else
+            sums(0);
     }
     float4 X[R];
     const float *from = nullptr;
@@ -234,19 +238,26 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         from = initial + ((size_t)sid * H + h) * D * D;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        X[r] = from != nullptr
+        X[r] = from != nullptr && adds
                    ? *reinterpret_cast<const float4 *>(from + (size_t)(x0 + r) * D + vs * VS + y0)
                    : make_float4(0.f, 0.f, 0.f, 0.f);
     double total = 0.0;
     for (int t = 0; t < n; ++t) {
         const int blk = block_of(t);
-        if (t + 1 < n) {
+        if (t + 1 < n && adds) {
             load(t + 1);
             cp_async_wait<1>();
         } else {
             cp_async_wait<0>();
         }
         __syncthreads();
+        if (!adds) {  // (meets the others at the block's three barriers)
+            total += sG[t & 1][C - 1];
+            if (t + 1 < n) sums(t + 1);
+            __syncthreads();
+            __syncthreads();
+            continue;
+        }
         const double *G = sG[t & 1];
         float *sa = tile_a(t), *sb = tile_b(t);
 #pragma unroll
@@ -265,7 +276,6 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         const double block_sum = G[C - 1];
         total += block_sum;
         __syncthreads();
-        if (tid < 32 && t + 1 < n) sums(t + 1);
         const float decay = expf((float)block_sum);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         to = seg_out + ((size_t)sg * H + h) * D * D;
     else if (fin != nullptr && s == (REV ? 0 : ns - 1))
         to = fin + ((size_t)sid * H + h) * D * D;
-    if (to != nullptr) {
+    if (to != nullptr && adds) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
             *reinterpret_cast<float4 *>(to + (size_t)(x0 + r) * D + vs * VS + y0) = X[r];

@@ -278,7 +278,7 @@ la_status gated_states_simt(const float *a, const float *b, const float *g, cons
     if (pl.segmented) {
         seg_state = reinterpret_cast<float *>(ws + pl.seg_state);
         seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
-        kern<<<grid, la::GatedSimt::THREADS, smem, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
+        kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
                                                          nullptr, nullptr, H, pl.tab);
         if (la_status st = launched(); st != LA_OK) return st;
         la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
@@ -286,7 +286,7 @@ la_status gated_states_simt(const float *a, const float *b, const float *g, cons
             D * D / 4, REV ? 1 : 0, pl.tab);
         if (la_status st = launched(); st != LA_OK) return st;
     }
-    kern<<<grid, la::GatedSimt::THREADS, smem, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
+    kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
                                                      H, pl.tab);
     return launched();
 }
