@@ -352,7 +352,7 @@ def state_prefix(gathered, rank: int, *, out=None, stream=None):
 
 
 def _is(t, name, dtype, dev):
-    """``_need`` with the usual case first: at one token a call's checks cost as much as its kernel."""
+    """``_need`` with the usual case first."""
     if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.device == dev and t.is_contiguous()):
         _need(t, name, dtype, dev)
 
@@ -367,11 +367,16 @@ def _stream_of(dev, stream):
     return _stream_ptr(stream)
 
 
-def _device_for(dev, stream):
-    """The context in which to call the library: ``_on_device`` where ``dev`` is not current already."""
+def _call(name, dev, stream, *args):
+    """One library call on ``dev``, whose last argument is the stream.  The device is switched
+    only where it is not current: at one token a call's checks cost as much as its kernel."""
     if stream is None and dev.type == "cuda" and torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return _on_device(dev, stream)
+        rc = getattr(lib(), name)(*args, _stream_of(dev, stream))
+    else:
+        with _on_device(dev, stream):
+            rc = getattr(lib(), name)(*args, _stream_of(dev, stream))
+    if rc != LA_OK:
+        _check(name, rc)
 
 
 def _gated_shape(q, k, v, g, cu_seqlens):
@@ -448,7 +453,7 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
     else:
         _need(out, "out", q.dtype, dev)
         _need_shape(out, "out", q.shape)
-        if any(_overlap(out, t) for t in (q, k, v, g) if t is not None):
+        if any(_overlap(out, t) for t in (q, k, v, g, initial_state) if t is not None):
             raise ValueError("out must not overlap an input")
     st = state_out
     if return_state and st is None:
@@ -461,13 +466,10 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
             raise ValueError("state_out and initial_state overlap without coinciding")
         if any(_overlap(st, t) for t in (q, k, v, g, out) if t is not None):
             raise ValueError("state_out must not overlap an input or out")
-    with _device_for(dev, stream):
-        ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 0, dev, stream)
-        rc = lib().la_gated_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr, num_seqs,
-                                    flags, _ptr(initial_state), _ptr(st), _ptr(ws), size,
-                                    _stream_of(dev, stream))
-        _check("la_gated_prefill", rc)
-        _used_on(stream, *made)
+    ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 0, dev, stream)
+    _call("la_gated_prefill", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr,
+          num_seqs, flags, _ptr(initial_state), _ptr(st), _ptr(ws), size)
+    _used_on(stream, *made)
     return (out, st) if st is not None else out
 
 
@@ -489,14 +491,11 @@ def gated_prefill_backward(q, k, v, g, do, *, cu_seqlens=None, initial_state=Non
     dq, dk, dv = (torch.empty_like(q) for _ in range(3))
     dg = None if g is None else torch.empty_like(g)
     d_init = None if initial_state is None else torch.empty_like(initial_state)
-    with _device_for(dev, stream):
-        ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 1, dev, stream)
-        rc = lib().la_gated_prefill_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), B, H, N, D,
-            cu_ptr, num_seqs, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init), _ptr(ws), size,
-            _stream_of(dev, stream))
-        _check("la_gated_prefill_backward", rc)
-        _used_on(stream, dq, dk, dv, dg, d_init)
+    ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 1, dev, stream)
+    _call("la_gated_prefill_backward", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(dq), _ptr(dk),
+          _ptr(dv), _ptr(dg), B, H, N, D, cu_ptr, num_seqs, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init),
+          _ptr(ws), size)
+    _used_on(stream, dq, dk, dv, dg, d_init)
     return (dq, dk, dv, dg) if d_init is None else (dq, dk, dv, dg, d_init)
 
 
@@ -505,9 +504,10 @@ def gated_decode_step(q, k, v, g, state, *, slots=None, out=None, stream=None):
 
     ``q, k, v``: ``[B, H, D]``; ``g``: ``[B, H]`` or ``None`` (no decay); ``state``:
     ``[num_slots, H, D, D]`` fp32.  ``slots`` (CUDA int32 ``[B]``): the slot of each row's
-    state, row ``b`` itself without it.  A row of slot -1 is padding: its state and its row
-    of ``o`` stay as they are.  A slot outside the pool, or the slot of an earlier row, is
-    skipped too, and ``device_status`` reports it.
+    state, row ``b`` itself without it.  A row of slot -1 is padding: no state is touched for
+    it, and its row of ``out`` stays as it is (without ``out``, as the allocator left it).  A
+    slot outside the pool, or the slot of an earlier row, is skipped too, and
+    ``device_status`` reports it.
     """
     _need(q, "q")
     shape, dtype, dev = q.shape, q.dtype, q.device
@@ -540,12 +540,10 @@ def gated_decode_step(q, k, v, g, state, *, slots=None, out=None, stream=None):
         _need_shape(out, "out", shape)
         if any(_overlap(out, t) for t in (q, k, v, g, state) if t is not None):
             raise ValueError("out must not overlap an input or the state")
-    with _device_for(dev, stream):
-        rc = lib().la_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), B, H, D,
-                                        _ptr(slots), num_slots, flags, _stream_of(dev, stream))
-        _check("la_gated_decode_step", rc)
-        if made:
-            _used_on(stream, out)
+    _call("la_gated_decode_step", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), B, H, D,
+          _ptr(slots), num_slots, flags)
+    if made:
+        _used_on(stream, out)
     return out
 
 
