@@ -14,14 +14,14 @@
 // two terms of dv take the places of s and t.  The decays of the first terms differ by row:
 // those of dq and dk are scaled in TMEM and the second products accumulate on top, the two of
 // dv are added on the way out.  Eight products, in this order:
-//   s, t; do S^T, v dS^T  ->  P, dP; scaling  ->  k dS; P^T do; dP k; dP^T q.
+//   t, v dS^T, s, do S^T  ->  P, dP; scaling  ->  k dS; P^T do; dP k; dP^T q.
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
 // Warps: 0 TMA loads and gate sums; 1 MMA issue; 2-9 (group A) scores -> P, dP, W, then dv and
 // dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out; 14 dg.
 // Every barrier completes one phase per block.  The next block's tiles are fetched into L2
-// while this one computes, loaded when its last product is done, and multiplied (s, t and the
+// while this one computes, loaded as their places come free, and multiplied (t, s and the
 // first terms) while its results go out.
 //
 // HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head
@@ -71,12 +71,12 @@ struct GatedBackwardCfg {
 };
 
 struct GatedBackwardMisc {
-    uint64_t full_qk, full_vo, full_ss;   // tiles landed
+    uint64_t full_vo, full_k, full_qs, full_ds;  // v, do; k; q, S; dS landed
     uint64_t gates;                       // gate sums of the block written
     uint64_t first_full;                  // s, t, do S^T, v dS^T
     uint64_t s_free;                      // group A has read s and t
     uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
-    uint64_t dv_full, dq_full, out_full;  // dv; dq; dk, and with it every product
+    uint64_t dv1_full, dv_full, dq_full, out_full;  // k dS; dv; dq; dk, and with it every product
     uint64_t dv_read, dq_read, dk_read;   // their accumulators have been read
     uint64_t dg_done;                     // the sums that dg is made of have been read
     uint64_t tail;                        // rows behind the sequence's end zeroed (blocks that have some)
@@ -121,9 +121,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     const int tiles = p.tab.blocks * p.H;
 
     if (tid == 0) {
-        mbar_init(&m->full_qk, 1);
         mbar_init(&m->full_vo, 1);
-        mbar_init(&m->full_ss, 1);
+        mbar_init(&m->full_k, 1);
+        mbar_init(&m->full_qs, 1);
+        mbar_init(&m->full_ds, 1);
+        mbar_init(&m->dv1_full, 1);
         mbar_init(&m->gates, 32);
         mbar_init(&m->first_full, 1);
         mbar_init(&m->dv_full, 1);
@@ -160,40 +162,49 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
-    int loads = 0;
-    auto load_tiles = [&](int x) {  // by a whole warp
+    // Loads by warp 0, each as soon as its place is free: dS once k dS is done, v and do once dv
+    // is, k once dq is, q and S once dk is.
+    int n_ds = 0, n_vo = 0, n_k = 0, n_qs = 0;
+    auto boxes = [&](int to, const CUtensorMap *map, int col, int row, int box, uint64_t *bar) {
+#pragma unroll 1
+        for (int d = 0; d < C::DB; ++d) tma_load_2d(sbase + to + d * box, map, col + 64 * d, row, bar);
+    };
+    auto place = [&](int x, int &row, int &col) {
         int rank, blk, start, len, sid;
         p.tab.block(x / p.H, rank, blk);
         p.tab.seqs.get(rank, start, len, sid);
-        const int row = start + blk * C::C, col = (x % p.H) * D;
-        ++loads;
+        row = start + blk * C::C;
+        col = (x % p.H) * D;
+    };
+    auto load_ds = [&](int x) {
+        ++n_ds;
         if (lane != 0) return;
-        mbar_arrive_expect_tx(&m->full_qk, 2 * C::TILE);
+        mbar_arrive_expect_tx(&m->full_ds, p.have_ds * C::DB * C::SBOX);
+        if (p.have_ds) boxes(C::OFF_DS, &p.tmap_ds, 0, x * D, C::SBOX, &m->full_ds);
+    };
+    auto load_vo = [&](int row, int col) {
+        ++n_vo;
+        if (lane != 0) return;
         mbar_arrive_expect_tx(&m->full_vo, 2 * C::TILE);
-        mbar_arrive_expect_tx(&m->full_ss, (p.have_s + p.have_ds) * C::DB * C::SBOX);
-#pragma unroll 1
-        for (int d = 0; d < C::DB; ++d) {
-            tma_load_2d(sbase + C::OFF_Q + d * C::BOX, &p.tmap_q, col + 64 * d, row, &m->full_qk);
-            tma_load_2d(sbase + C::OFF_K + d * C::BOX, &p.tmap_k, col + 64 * d, row, &m->full_qk);
-        }
-#pragma unroll 1
-        for (int d = 0; d < C::DB; ++d) {
-            tma_load_2d(sbase + C::OFF_DO + d * C::BOX, &p.tmap_do, col + 64 * d, row, &m->full_vo);
-            tma_load_2d(sbase + C::OFF_V + d * C::BOX, &p.tmap_v, col + 64 * d, row, &m->full_vo);
-        }
-#pragma unroll 1
-        for (int d = 0; d < C::DB; ++d) {
-            if (p.have_s) tma_load_2d(sbase + C::OFF_S + d * C::SBOX, &p.tmap_s, 64 * d, x * D, &m->full_ss);
-            if (p.have_ds) tma_load_2d(sbase + C::OFF_DS + d * C::SBOX, &p.tmap_ds, 64 * d, x * D, &m->full_ss);
-        }
+        boxes(C::OFF_DO, &p.tmap_do, col, row, C::BOX, &m->full_vo);
+        boxes(C::OFF_V, &p.tmap_v, col, row, C::BOX, &m->full_vo);
+    };
+    auto load_k = [&](int row, int col) {
+        ++n_k;
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(&m->full_k, C::TILE);
+        boxes(C::OFF_K, &p.tmap_k, col, row, C::BOX, &m->full_k);
+    };
+    auto load_qs = [&](int x, int row, int col) {
+        ++n_qs;
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(&m->full_qs, C::TILE + p.have_s * C::DB * C::SBOX);
+        boxes(C::OFF_Q, &p.tmap_q, col, row, C::BOX, &m->full_qs);
+        if (p.have_s) boxes(C::OFF_S, &p.tmap_s, 0, x * D, C::SBOX, &m->full_qs);
     };
     // The next tile's data into L2 while this one computes: shared memory is full, so that its
     // loads can only start when this tile's last product is done.
-    auto prefetch = [&](int x) {
-        int rank, blk, start, len, sid;
-        p.tab.block(x / p.H, rank, blk);
-        p.tab.seqs.get(rank, start, len, sid);
-        const int row = start + blk * C::C, col = (x % p.H) * D;
+    auto prefetch = [&](int x, int row, int col) {
         if (lane != 0) return;
 #pragma unroll 1
         for (int d = 0; d < C::DB; ++d) {
@@ -213,15 +224,21 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         fetch_gates4(raw, p.g, start + blk * C::C, min(C::C, len - blk * C::C), p.H, x % p.H);
     };
     if (warp == 0 && (int)blockIdx.x < tiles) {
-        load_tiles(blockIdx.x);
+        int row, col;
+        place(blockIdx.x, row, col);
+        load_vo(row, col);
+        load_k(row, col);
+        load_qs(blockIdx.x, row, col);
+        load_ds(blockIdx.x);
         fetch(blockIdx.x);
     }
     const uint32_t leader = elect_leader();
     bool ok = true;
     // Phase of the block's barriers, of the block before, and of `tail`.  Every wait is exact: no
-    // barrier's next phase completes before all who wait for this one have returned.  Loads of
-    // the next block need out_full, hence p_ready and scaled, hence groups A's and B's waits;
-    // its products need dv_read, dq_read and dk_read; its sums (p_ready, scaled) dg_done.
+    // barrier's next phase completes before all who wait for this one have returned.  Each load
+    // of the next block needs a product of this one behind p_ready, hence group A's waits (and
+    // the last one scaled, hence group B's); the next block's products need dv_read, dq_read and
+    // dk_read; its sums (p_ready, scaled) dg_done.
     uint32_t ph = 0, tail_ph = 0;
     for (int x = blockIdx.x; ok && x < tiles; x += gridDim.x, ph ^= 1u) {
         const int h = x % p.H;
@@ -239,7 +256,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             mbar_arrive(&m->gates);
             if (tail) {
                 // rows of the next sequence must not enter any sum over the block's tokens
-                ok = wwait(&m->full_qk, ph) && wwait(&m->full_vo, ph);
+                ok = wwait(&m->full_qs, ph) && wwait(&m->full_k, ph) && wwait(&m->full_vo, ph);
                 if (!ok) break;
                 for (int t = 0; t < 4 * C::DB; ++t)
                     for (int c = nv * 8 + lane; c < C::C * 8; c += 32)
@@ -248,11 +265,15 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 mbar_arrive(&m->tail);
             }
             if (next < tiles) {
+                int row, col;
+                place(next, row, col);
                 fetch(next);
-                prefetch(next);
+                prefetch(next, row, col);
+                if ((ok = wwait(&m->dv1_full, ph))) load_ds(next);
+                if (ok && (ok = wwait(&m->dv_full, ph))) load_vo(row, col);
+                if (ok && (ok = wwait(&m->dq_full, ph))) load_k(row, col);
+                if (ok && (ok = wwait(&m->out_full, ph))) load_qs(next, row, col);
             }
-            ok = wwait(&m->out_full, ph);
-            if (ok && next < tiles) load_tiles(next);  // every product that reads the tiles is done
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issue
@@ -271,27 +292,27 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             };
             const uint64_t qk = desc_kmajor_sw128(sbase + C::OFF_Q), kkd = desc_kmajor_sw128(sbase + C::OFF_K),
                            vk = desc_kmajor_sw128(sbase + C::OFF_V), ok_ = desc_kmajor_sw128(sbase + C::OFF_DO);
-            ok = wwait(&m->full_qk, ph) && (!tail || wwait(&m->tail, tail_ph)) && (first || wwait(&m->dv_read, ph ^ 1u));
-            if (ok) {
-                tc_fence_after();
-                product(C::TM_S, qk, kk, kkd, kk, C::ID_S, D / 16, false);
-                ok = wwait(&m->full_vo, ph);
-            }
+            ok = wwait(&m->full_vo, ph) && (!tail || wwait(&m->tail, tail_ph)) && (first || wwait(&m->dv_read, ph ^ 1u));
             if (ok) {
                 tc_fence_after();
                 product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
-                ok = wwait(&m->full_ss, ph) && (first || wwait(&m->dq_read, ph ^ 1u));
-            }
-            if (ok) {
-                tc_fence_after();
-                if (p.have_s)
-                    product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
-                ok = first || wwait(&m->dk_read, ph ^ 1u);
+                ok = wwait(&m->full_ds, ph) && (first || wwait(&m->dk_read, ph ^ 1u));
             }
             if (ok) {
                 tc_fence_after();
                 if (p.have_ds)
                     product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
+                ok = wwait(&m->full_k, ph) && wwait(&m->full_qs, ph);
+            }
+            if (ok) {
+                tc_fence_after();
+                product(C::TM_S, qk, kk, kkd, kk, C::ID_S, D / 16, false);
+                ok = first || wwait(&m->dq_read, ph ^ 1u);
+            }
+            if (ok) {
+                tc_fence_after();
+                if (p.have_s)
+                    product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
                 warp_commit(leader, &m->first_full);
                 ok = wwait(&m->s_free, ph);
             }
@@ -300,6 +321,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 if (p.have_ds)
                     product(C::TM_DV1, kkd, kk, desc_mnmajor_sw128(sbase + C::OFF_DS, C::SBOX), nn, C::ID_KN, D / 16,
                             false);
+                warp_commit(leader, &m->dv1_full);
                 ok = wwait(&m->p_ready, ph);
             }
             if (ok) {
@@ -414,6 +436,10 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             tmem_ld16(tmem + C::TM_S + 16 * pc + lanes, sc);
                             tmem_ld16(tmem + C::TM_T + 16 * pc + lanes, t);
                             tmem_ld_wait();
+                            if (pc >= 2 * q) {  // the warp's last columns of s and t
+                                tc_fence_before();
+                                mbar_arrive(&m->s_free);
+                            }
                             uint64_t w2[8], sum2 = 0;          // W in pairs of columns
 #pragma unroll
                             for (int y = 0; y < 16; y += 4) {
@@ -462,8 +488,6 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             st_shared_v4(C::OFF_DP + o, dP[4 * c], dP[4 * c + 1], dP[4 * c + 2], dP[4 * c + 3]);
                         }
                     }
-                    tc_fence_before();
-                    mbar_arrive(&m->s_free);
                     sRow[128 * half + i] = row;
                     fence_proxy_async_smem();
                     mbar_arrive(&m->p_ready);
@@ -483,7 +507,8 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             } else {
                 // -------------------------------------------------------- group B: first terms
                 float r = 0.f, e = 0.f;
-                ok = wwait(&m->gates, ph) && wwait(&m->full_qk, ph) && wwait(&m->first_full, ph) &&
+                ok = wwait(&m->gates, ph) && wwait(&m->full_qs, ph) && wwait(&m->full_k, ph) &&
+                     wwait(&m->first_full, ph) &&
                      (!tail || wwait(&m->tail, tail_ph)) && (first || wwait(&m->dg_done, ph ^ 1u));
                 if (ok) {
                     tc_fence_after();
@@ -537,11 +562,13 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     }
     if (!ok) fail();
     if (warp == 0 && !ok) {  // loads that are still in flight land before the CTA ends
-        if (loads > 0) {
-            mbar_wait(&m->full_qk, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
-            mbar_wait(&m->full_vo, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
-            mbar_wait(&m->full_ss, (uint32_t)((loads - 1) & 1), nullptr, tlimit);
-        }
+        auto landed = [&](uint64_t *bar, int n) {
+            if (n > 0) mbar_wait(bar, (uint32_t)((n - 1) & 1), nullptr, tlimit);
+        };
+        landed(&m->full_ds, n_ds);
+        landed(&m->full_vo, n_vo);
+        landed(&m->full_k, n_k);
+        landed(&m->full_qs, n_qs);
     }
     if (warp == 1) {  // every issued MMA has finished before TMEM is freed
         warp_commit(leader, &m->done);
