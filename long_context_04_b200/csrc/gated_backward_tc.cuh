@@ -36,7 +36,7 @@ struct GatedBackwardParams {
     CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;  // [T][H*D], box 64 x 128
     CUtensorMap tmap_s, tmap_ds;                  // [blocks * H * D][D], box 64 x D
     const __nv_bfloat16 *g;
-    const float *through;  // [blocks][H][4 D / 64] parts of e^{G_C} <dS, S>, or nullptr
+    const float *through;  // [blocks][H][8 D / 64] parts of e^{G_C} <dS, S>, or nullptr
     __nv_bfloat16 *dq, *dk, *dv, *dg;
     int H;
     int have_s, have_ds;   // snapshots of the state, of its gradient (else zero)
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         } else if (warp == 14) {
             // ------------------------------------------------------------ dg
             float part = 0.f;
-            if (p.through != nullptr && lane < 4 * C::DB) part = p.through[(size_t)x * (4 * C::DB) + lane];
+            if (p.through != nullptr && lane < 8 * C::DB) part = p.through[(size_t)x * (8 * C::DB) + lane];
             ok = wwait(&m->p_ready, ph) && wwait(&m->scaled, ph);
             if (!ok) break;
             float r[4], e[4], up[4], down[4];
@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 e[y] = sE[t] + (((sCol[t] + sCol[128 + t]) + (sCol[256 + t] + sCol[384 + t])) -
                                 (sRow[t] + sRow[128 + t]));
             }
+            reads_done();
             mbar_arrive(&m->dg_done);
             if (p.dg != nullptr) {
                 // dg_t = e^{G_C} <dS, S> + sum_{i >= t} sR_i + sum_{j < t} (sE_j + col_j - row_j)

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(GatedPrefillCfg<D>::THREADS, 1)
     // says so, and gates_ready of b + 2 needs that of every warp
     auto sums_of = [&](int b) { return reinterpret_cast<float *>(smem + C::OFF_G) + C::C * (b & 1); };
     auto gates_read = [&](int b) {
+        reads_done();
         __syncwarp();
         if (lane == 0) mbar_arrive(&m->gates_free[b & 1]);
     };

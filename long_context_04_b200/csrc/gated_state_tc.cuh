@@ -19,11 +19,13 @@
 // tile is read by D / 64 CTAs, mostly from L2) and 2 D^2 / 128 bytes of snapshot written per
 // token and head.
 //
-// Warpgroups (512 threads; registers are moved to the one that holds the state):
+// Warpgroups (640 threads; registers are moved to those that hold the state):
 //   0  warp 0 loads of the tiles; warp 1 MMA issue; warp 2 gate sums; warp 3 loads of the forward
 //      snapshots (reverse scan)
-//   1  epilogue: the state, its snapshots, in the reverse scan the parts of e^{G_C} <X, state>
-//   2, 3  scaling
+//   1, 2  epilogue, 32 columns each: the state, its snapshots, in the reverse scan the parts of
+//      e^{G_C} <X, state>.  (Its chain of one block after the other is what bounds the scan: with
+//      one warpgroup for all 64 columns a block took 1.4 us forward and 1.8 us in reverse.)
+//   3, 4  scaling
 #pragma once
 
 #include "gated.cuh"
@@ -42,7 +44,7 @@ struct GatedStateParams {
     CUtensorMap tmap_snap;      // snapshots, [blocks * H * D][D], box 64 x D
     CUtensorMap tmap_other;     // reverse: the forward snapshots, the same
     int have_snap;
-    float *through;             // reverse: [blocks][H][4 D / 64] parts of e^{G_C} <X, state>, or nullptr
+    float *through;             // reverse: [blocks][H][8 D / 64] parts of e^{G_C} <X, state>, or nullptr
     int H;
     unsigned long long timeout_ns;
     GatedTable tab;
@@ -68,10 +70,10 @@ struct GatedStateCfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static constexpr int TMEM_COLS = 256;           // two accumulators of 128 columns
     static constexpr int ACC = 128;
-    static constexpr int GROUP = 128, THREADS = 4 * GROUP;
-    // registers a thread: launched with 128; the shares of the four warpgroups add up to 4 * 128
-    static constexpr int R_LAUNCH = 128, R_MISC = 64, R_STATE = 224, R_SCALE = 112;
-    static_assert(R_MISC + R_STATE + 2 * R_SCALE == 4 * R_LAUNCH, "register shares");
+    static constexpr int GROUP = 256, THREADS = 128 + 2 * GROUP;  // threads of the epilogue, of scaling
+    // registers a thread: launched with 96; the shares of the five warpgroups add up to 5 * 96
+    static constexpr int R_LAUNCH = 96, R_MISC = 56, R_STATE = 128, R_SCALE = 80;
+    static_assert(R_MISC + 2 * R_STATE + 2 * R_SCALE <= 5 * R_LAUNCH, "register shares");
     static constexpr uint32_t ID2 = idesc_bf16_f32(D, 128, 1, 1), ID1 = idesc_bf16_f32(D, 64, 1, 1);
 };
 
@@ -347,6 +349,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "r"(addr));
     return r;
 }
+// What this thread has read from shared memory so far has been read: behind it an arrival may
+// give the place away.  The arrival alone does not see to that: loads were found to take
+// place behind it, after the place had been refilled.
+__device__ __forceinline__ void reads_done() { __threadfence_block(); }
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4 &v) {
     st_shared_v4(addr, v.x, v.y, v.z, v.w);
 }
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             mbar_init(&m->acc_full[i], 1);
             mbar_init(&m->acc_free[i], C::GROUP);
             mbar_init(&m->gates_ready[i], 32);
-            mbar_init(&m->gates_free[i], 12);  // the warps of the epilogue and of scaling
+            mbar_init(&m->gates_free[i], 16);  // the warps of the epilogue and of scaling
         }
         mbar_init(&m->done, 1);
         m->abort_flag = 0;
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             if (!ok) fail();
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ---------------------------------------------------------------- epilogue: the state
         reg_inc<C::R_STATE>();
         const int q = warp & 3;
@@ -518,30 +524,32 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
         const int i = D == 128 ? 32 * q + lane : 16 * q + lane;
         const bool i_ok = D == 128 || lane < 16;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-        float X[64];  // X[i][64 vs .. 64 vs + 63]
+        const int cg = (warp - 4) >> 2, col = 64 * vs + 32 * cg;  // this thread's columns of the state
+        float X[32];  // X[i][col .. col + 31]
 #pragma unroll
-        for (int x = 0; x < 64; ++x) X[x] = 0.f;
+        for (int x = 0; x < 32; ++x) X[x] = 0.f;
         const float *from = nullptr;
         if (p.seg_in != nullptr)
             from = p.seg_in + ((size_t)sg * p.H + h) * D * D;
         else if (p.initial != nullptr)
             from = p.initial + ((size_t)sid * p.H + h) * D * D;
         if (from != nullptr && i_ok) {
-            const float4 *src = reinterpret_cast<const float4 *>(from + (size_t)i * D + 64 * vs);
+            const float4 *src = reinterpret_cast<const float4 *>(from + (size_t)i * D + col);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < 8; ++x) {
                 const float4 f = src[x];
                 X[4 * x] = f.x, X[4 * x + 1] = f.y, X[4 * x + 2] = f.z, X[4 * x + 3] = f.w;
             }
         }
         // reverse: this row of the block's forward snapshot, read a block ahead, so that the one
         // place for it is refilled meanwhile
-        uint4 o[8];
+        uint4 o[4];
         auto take_other = [&](int t) -> bool {
             if (!wwait(&m->other_full, one(t))) return false;
             const uint32_t at = sbase + C::OFF_OTHER + (i_ok ? i : 0) * 128;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) o[x] = ld_shared_v4(at + ((x ^ (i & 7)) << 4));
+            for (int x = 0; x < 4; ++x) o[x] = ld_shared_v4(at + (((4 * cg + x) ^ (i & 7)) << 4));
+            fence_proxy_async_smem();  // the rows have been read (reads_done), and TMA may write
             mbar_arrive(&m->other_free);
             return true;
         };
@@ -554,6 +562,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             if (ok) ok = wwait(&m->gates_ready[t & 1], two(t));
             const float G = m->sum[t & 1], decay = exp2f(G);
             if (ok) {
+                reads_done();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->gates_free[t & 1]);
                 total += G;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
+                for (int x = 0; x < 4; ++x) {
                     const uint32_t in[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -573,7 +582,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 float f = i_ok ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
-                if (lane == 0) p.through[(size_t)number_of(t) * (4 * C::NVS) + 4 * vs + q] = decay * f;
+                if (lane == 0) p.through[(size_t)number_of(t) * (8 * C::NVS) + 8 * vs + 4 * cg + q] = decay * f;
             }
             if (p.have_snap) {
                 // bf16 rows into one of two buffers, whose store of two blocks ago has read it; then
@@ -584,8 +593,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 const uint32_t at = sbase + C::OFF_SNAP + (t & 1) * C::SBOX;
                 if (i_ok) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        st_shared_u4(at + i * 128 + ((x ^ (i & 7)) << 4), pack_chunk(&X[8 * x]));
+                    for (int x = 0; x < 4; ++x)
+                        st_shared_u4(at + i * 128 + (((4 * cg + x) ^ (i & 7)) << 4), pack_chunk(&X[8 * x]));
                 }
                 fence_proxy_async_smem();
                 named_barrier(1, C::GROUP);
@@ -598,21 +607,16 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             if (ok) ok = wwait(&m->acc_full[t & 1], two(t));
             if (ok) {
                 tc_fence_after();
-                const uint32_t tA = tmem + C::ACC * (t & 1) + lane_base;
+                const uint32_t tA = tmem + C::ACC * (t & 1) + 32 * cg + lane_base;
+                uint32_t a[32], c[32];
+                tmem_ld32(tA, a);
+                tmem_ld32(tA + 64, c);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(&m->acc_free[t & 1]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t a[32], c[32];
-                    tmem_ld32(tA + 32 * x, a);
-                    tmem_ld32(tA + 64 + 32 * x, c);
-                    tmem_ld_wait();
-                    if (x == 1) {
-                        tc_fence_before();
-                        mbar_arrive(&m->acc_free[t & 1]);
-                    }
-#pragma unroll
-                    for (int z = 0; z < 32; ++z)
-                        X[32 * x + z] = fmaf(decay, X[32 * x + z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
-                }
+                for (int z = 0; z < 32; ++z)
+                    X[z] = fmaf(decay, X[z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
             }
             if (ok && through && t + 1 < nb) ok = take_other(t + 1);
         }
@@ -623,17 +627,17 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
         else if (p.fin != nullptr && s == (REV ? 0 : p.tab.num_segs(rank) - 1))
             to = p.fin + ((size_t)sid * p.H + h) * D * D;
         if (ok && to != nullptr && i_ok) {
-            float4 *d4 = reinterpret_cast<float4 *>(to + (size_t)i * D + 64 * vs);
+            float4 *d4 = reinterpret_cast<float4 *>(to + (size_t)i * D + col);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) d4[x] = make_float4(X[4 * x], X[4 * x + 1], X[4 * x + 2], X[4 * x + 3]);
+            for (int x = 0; x < 8; ++x) d4[x] = make_float4(X[4 * x], X[4 * x + 1], X[4 * x + 2], X[4 * x + 3]);
         }
-        if (ok && p.seg_out != nullptr && vs == 0 && q == 0 && lane == 0)
+        if (ok && p.seg_out != nullptr && vs == 0 && warp == 4 && lane == 0)
             p.seg_total[(size_t)sg * p.H + h] = total * 0.6931471805599453f;
         if (!ok) fail();
     } else {
         // ---------------------------------------------------------------- scaling: 16 rows a warp
         reg_dec<C::R_SCALE>();
-        const int w8 = warp - 8, u = w8 >> 1;
+        const int w8 = warp - 12, u = w8 >> 1;
         bool ok = true;
         for (int t = 0; t < nb; ++t) {
             const int nv = rows_of(t);

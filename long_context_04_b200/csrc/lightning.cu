@@ -256,7 +256,7 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
     pl.snap = take(tc && !backward ? 0 : (size_t)nblk * H * shot);
     pl.dsnap = take(backward ? (size_t)nblk * H * shot : 0);
-    pl.through = take(tc && backward ? (size_t)nblk * H * 4 * slices * 4 : 0);
+    pl.through = take(tc && backward ? (size_t)nblk * H * 8 * slices * 4 : 0);
     pl.seg_state = take(pl.segmented ? (size_t)nseg * H * state : 0);
     pl.seg_total = take(pl.segmented ? (size_t)nseg * H * 4 : 0);
     pl.bytes = at;
