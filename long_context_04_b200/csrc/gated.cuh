@@ -95,7 +95,8 @@ __device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.
 // out = start states of a (sequence, head)'s segments from their own end states, in order:
 //     X_0 = initial, X_{s+1} = e^{total_s} X_s + local_s;   seg_state[s] <- X_s.
 // `rev` walks the segments from the last to the first (the state's gradient).  One thread
-// per float4 of the state; grid (S * H, D * D / 1024).
+// per float4 of the state; grid (S * H, D * D / 1024).  Latency-bound: eight segments' loads
+// are in flight at once.
 __global__ void __launch_bounds__(256)
     gated_prefix_kernel(float4 *__restrict__ seg_state, const float *__restrict__ seg_total,
                         const float4 *__restrict__ initial, int H, int n4, int rev,
@@ -174,7 +175,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // segment starts from seg_in (segmented call) or the sequence's initial state; seg_out and
 // seg_total take a segment's own end state and decay; fin the sequence's final state.
 // The next block's tiles come by cp.async while this one is added up: a block of few heads is
-// all latency (64 x 64 x 32 products a CTA).
+// all latency (64 x 64 x 32 products a CTA; about 3 us a block).
 template <int D>
 struct GatedStateSimt {
     static constexpr int A = GatedSimt::C * D, B = GatedSimt::C * GatedSimt::VS;
@@ -505,7 +506,9 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 }
 
 // Gradients of one block of one head, from the state at its start (snap) and the state's
-// gradient at its end (dsnap); either may be nullptr for zero.
+// gradient at its end (dsnap); either may be nullptr for zero.  Bound by FMA issue and the
+// shared-memory loads that feed it; a call of 1000 tokens of 4 heads, D = 64, takes 113 us, of
+// which the two scans' chains of 16 blocks are the larger part.
 template <int D>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
     gated_backward_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
@@ -660,20 +663,70 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
 }
 
 // ------------------------------------------------------------------ one token
-// state <- e^g state + k v^T, o = state^T q for one token per row, the state in slot
-// slots[b] of a pool of num_slots (row b itself without slots).  One CTA of 256 threads per
-// (row, head), as the plain decode step: HBM-bound, 8 D^2 bytes against 6 D^2 flops.
+// state_out <- e^g state_in + k v^T, o = state_out^T q for one token of one head, by 256
+// threads.  Without state_in the state before was zero; without state_out it is not kept
+// (BOTH: both are there, which spares a full batch 1.5 % of its time).
+template <int D, typename T, bool BOTH>
+__device__ __forceinline__ void gated_one_token(const T *__restrict__ q, const T *__restrict__ k,
+                                                const T *__restrict__ v, const T *__restrict__ g, T *__restrict__ o,
+                                                const float4 *state_in, float4 *state_out) {
+    constexpr int C4 = D / 4, RG = 256 / C4, RPT = D / RG;
+    __shared__ float sq[D], sk[D];
+    __shared__ float red[RG][D];
+    const int tid = threadIdx.x, c4 = tid % C4, rg = tid / C4;
+    float4 x[RPT];
+#pragma unroll
+    for (int t = 0; t < RPT; ++t)
+        x[t] = BOTH || state_in != nullptr ? __ldcs(&state_in[(size_t)(rg + RG * t) * C4 + c4])
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < D) {
+        sq[tid] = to_f32(q[tid]);
+        sk[tid] = to_f32(k[tid]);
+    }
+    const float a = g != nullptr ? expf(clamp_gate(to_f32(*g))) : 1.f;
+    const float v0 = to_f32(v[4 * c4]), v1 = to_f32(v[4 * c4 + 1]), v2 = to_f32(v[4 * c4 + 2]),
+                v3 = to_f32(v[4 * c4 + 3]);
+    __syncthreads();
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+    for (int t = 0; t < RPT; ++t) {
+        const int r = rg + RG * t;
+        const float kr = sk[r], qr = sq[r];
+        x[t].x = fmaf(kr, v0, a * x[t].x);
+        x[t].y = fmaf(kr, v1, a * x[t].y);
+        x[t].z = fmaf(kr, v2, a * x[t].z);
+        x[t].w = fmaf(kr, v3, a * x[t].w);
+        if (BOTH || state_out != nullptr) __stcs(&state_out[(size_t)r * C4 + c4], x[t]);
+        a0 = fmaf(qr, x[t].x, a0);
+        a1 = fmaf(qr, x[t].y, a1);
+        a2 = fmaf(qr, x[t].z, a2);
+        a3 = fmaf(qr, x[t].w, a3);
+    }
+    red[rg][4 * c4 + 0] = a0;
+    red[rg][4 * c4 + 1] = a1;
+    red[rg][4 * c4 + 2] = a2;
+    red[rg][4 * c4 + 3] = a3;
+    __syncthreads();
+    if (tid < D) {
+        float out = 0.f;
+#pragma unroll
+        for (int y = 0; y < RG; ++y) out += red[y][tid];
+        o[tid] = from_f32<T>(out);
+    }
+}
+
+// One token per row, the state in slot slots[b] of a pool of num_slots (row b itself without
+// slots), updated in place.  One CTA of 256 threads per
+// (row, head), as the plain decode step: HBM-bound, 8 D^2 bytes against 6 D^2 flops (256 rows,
+// 64 heads, D = 128: 335 us, 6.5 TB/s; one row 3.5 us).
 // A row of slot -1 is padding: nothing of it is read or written.  A slot outside the pool,
 // or one that an earlier row of the batch has (two rows would race for one state), is
 // skipped in the same way and recorded as DEV_RANGE.
 template <int D, typename T>
 __global__ void __launch_bounds__(256)
     gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                        const T *__restrict__ g, float *__restrict__ state, T *__restrict__ o, int H,
+                        const T *__restrict__ g, float *state, T *__restrict__ o, int H,
                         const int *__restrict__ slots, int num_slots) {
-    constexpr int C4 = D / 4, RG = 256 / C4, RPT = D / RG;
-    __shared__ float sq[D], sk[D];
-    __shared__ float red[RG][D];
     const int b = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x;
     const size_t vec = (size_t)blockIdx.x * D;
     int slot = b;
@@ -691,44 +744,23 @@ __global__ void __launch_bounds__(256)
         }
     }
     float4 *S = reinterpret_cast<float4 *>(state + ((size_t)slot * H + h) * D * D);
-    const int c4 = tid % C4, rg = tid / C4;
-    float4 x[RPT];
-#pragma unroll
-    for (int t = 0; t < RPT; ++t) x[t] = __ldcs(&S[(size_t)(rg + RG * t) * C4 + c4]);
-    if (tid < D) {
-        sq[tid] = to_f32(q[vec + tid]);
-        sk[tid] = to_f32(k[vec + tid]);
-    }
-    const float a = g != nullptr ? expf(clamp_gate(to_f32(g[blockIdx.x]))) : 1.f;
-    const float v0 = to_f32(v[vec + 4 * c4]), v1 = to_f32(v[vec + 4 * c4 + 1]),
-                v2 = to_f32(v[vec + 4 * c4 + 2]), v3 = to_f32(v[vec + 4 * c4 + 3]);
-    __syncthreads();
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-    for (int t = 0; t < RPT; ++t) {
-        const int r = rg + RG * t;
-        const float kr = sk[r], qr = sq[r];
-        x[t].x = fmaf(kr, v0, a * x[t].x);
-        x[t].y = fmaf(kr, v1, a * x[t].y);
-        x[t].z = fmaf(kr, v2, a * x[t].z);
-        x[t].w = fmaf(kr, v3, a * x[t].w);
-        __stcs(&S[(size_t)r * C4 + c4], x[t]);
-        a0 = fmaf(qr, x[t].x, a0);
-        a1 = fmaf(qr, x[t].y, a1);
-        a2 = fmaf(qr, x[t].z, a2);
-        a3 = fmaf(qr, x[t].w, a3);
-    }
-    red[rg][4 * c4 + 0] = a0;
-    red[rg][4 * c4 + 1] = a1;
-    red[rg][4 * c4 + 2] = a2;
-    red[rg][4 * c4 + 3] = a3;
-    __syncthreads();
-    if (tid < D) {
-        float out = 0.f;
-#pragma unroll
-        for (int y = 0; y < RG; ++y) out += red[y][tid];
-        o[vec + tid] = from_f32<T>(out);
-    }
+    gated_one_token<D, T, true>(q + vec, k + vec, v + vec, g != nullptr ? g + blockIdx.x : nullptr, o + vec, S, S);
+}
+
+// The sequences of one token of a packed call, rows of the packed arrays in place: the
+// state from the sequence's initial state (or zero) to its final state (or nowhere).  256 of
+// them, 64 heads, D = 128, take 318 us here; as blocks of the prefill kernel they took 1844.
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+    gated_rows_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                      const T *__restrict__ g, T *__restrict__ o, const float *initial, float *fin, int H,
+                      const __grid_constant__ OneTokenTable tab) {
+    const int i = blockIdx.x / H, h = blockIdx.x % H;
+    const size_t row = (size_t)(tab.identity ? i : tab.row[i]) * H + h;
+    const size_t state = ((size_t)(tab.identity ? i : tab.sid[i]) * H + h) * D * D;
+    gated_one_token<D, T, false>(q + row * D, k + row * D, v + row * D, g != nullptr ? g + row : nullptr, o + row * D,
+                                 initial != nullptr ? reinterpret_cast<const float4 *>(initial + state) : nullptr,
+                                 fin != nullptr ? reinterpret_cast<float4 *>(fin + state) : nullptr);
 }
 
 }  // namespace la

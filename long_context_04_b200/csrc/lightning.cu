@@ -171,6 +171,10 @@ struct GatedPlan {
     GatedTable tab;
     bool segmented;
     int longest;                   // blocks of the longest sequence
+    // prefill: the sequences of one token, which are decode steps and not in the table (one
+    // would hold a whole CTA per slice for one row)
+    la::OneTokenTable one;
+    int ones;
     // workspace offsets (bytes): state snapshots of both directions, the parts of <dS, S>,
     // segment states, their decays
     size_t snap, dsnap, through, seg_state, seg_total, bytes;
@@ -193,11 +197,32 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     const bool tc = (flags & LA_BF16) != 0;
     const int C = tc ? 128 : la::GatedSimt::C, slices = tc ? D / 64 : D / la::GatedSimt::VS;
     const int resident = kSMs, min_seg = 4;
+    pl.ones = pl.one.identity = 0;
+    if (!backward) {
+        if (t.seqs.varlen) {
+            int w = 0;
+            for (int r = 0; r < S; ++r) {
+                if (t.seqs.seq_len[r] == 1) {
+                    pl.one.row[pl.ones] = t.seqs.seq_start[r];
+                    pl.one.sid[pl.ones++] = t.seqs.seq_id[r];
+                } else {
+                    t.seqs.seq_start[w] = t.seqs.seq_start[r];
+                    t.seqs.seq_len[w] = t.seqs.seq_len[r];
+                    t.seqs.seq_id[w++] = t.seqs.seq_id[r];
+                }
+            }
+            S = w;
+        } else if (N == 1) {
+            pl.one.identity = 1;
+            pl.ones = S;
+            S = 0;
+        }
+    }
     t.S = S;
     t.C = C;
     long long blocks = 0;
     pl.longest = 0;
-    for (int r = 0; r < (t.seqs.varlen ? S : 1); ++r) {
+    for (int r = 0; r < (t.seqs.varlen ? S : std::min(S, 1)); ++r) {
         const int nb = ((t.seqs.varlen ? t.seqs.seq_len[r] : N) + C - 1) / C;
         pl.longest = std::max(pl.longest, nb);
         blocks += t.seqs.varlen ? nb : (long long)nb * S;
@@ -244,7 +269,9 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         nseg = (long long)S * t.segs_per_seq;
     }
     // (the snapshots' rows, nblk * H * D, are coordinates of a tensor map)
-    if (T >= (1ll << 31) || nblk * H * D >= (1ll << 31) || nseg * H * slices >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
+    if (T >= (1ll << 31) || nblk * H * D >= (1ll << 31) || nseg * H * slices >= (1ll << 31) ||
+        (long long)pl.ones * H >= (1ll << 31))
+        return LA_ERR_UNSUPPORTED;
     t.blocks = (int)nblk;
     t.segs = (int)nseg;
     size_t at = 0;
@@ -264,6 +291,16 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
 }
 
 la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
+
+// The sequences of one token of a prefill call.
+template <int D, typename E>
+la_status gated_rows(const void *q, const void *k, const void *v, const void *g, void *o, const float *state_in,
+                     float *state_out, int H, const GatedPlan &pl, cudaStream_t stream) {
+    la::gated_rows_kernel<D, E><<<(unsigned)(pl.ones * H), 256, 0, stream>>>(
+        static_cast<const E *>(q), static_cast<const E *>(k), static_cast<const E *>(v), static_cast<const E *>(g),
+        static_cast<E *>(o), state_in, state_out, H, pl.one);
+    return launched();
+}
 
 // State scan of one direction: snapshots per block, the final state where wanted.
 template <int D, bool REV>
@@ -301,6 +338,7 @@ la_status gated_prefill_simt(const float *q, const float *k, const float *v, con
         if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
             st != LA_OK)
             return st;
+    if (pl.tab.blocks == 0) return LA_OK;  // beside sequences of one token only empty ones
     auto kern = la::gated_prefill_simt_kernel<D>;
     constexpr int smem = la::GatedSimtTiles<D>::FWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -809,6 +847,12 @@ la_status la_gated_prefill(const void *q, const void *k, const void *v, const vo
     if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (T == 0) return gated_no_tokens(state_in, state_out, pl.tab.S, H, D, stream);
+    if (pl.ones > 0) {
+        auto *rows = (flags & LA_BF16) ? (D == 128 ? gated_rows<128, __nv_bfloat16> : gated_rows<64, __nv_bfloat16>)
+                                       : (D == 128 ? gated_rows<128, float> : gated_rows<64, float>);
+        if (la_status st = rows(q, k, v, g, o, state_in, state_out, H, pl, stream); st != LA_OK || pl.tab.S == 0)
+            return st;
+    }
     if (flags & LA_BF16) {
         if (D == 128) return gated_prefill_tc<128>(q, k, v, g, o, state_in, state_out, H, T, pl, ws, stream);
         return gated_prefill_tc<64>(q, k, v, g, o, state_in, state_out, H, T, pl, ws, stream);

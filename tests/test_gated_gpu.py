@@ -181,6 +181,33 @@ def test_many_short_sequences(dtype):
     assert rel(p, ref) <= out_tol(dtype)
 
 
+@pytest.mark.parametrize("dtype,D", KINDS, ids=IDS)
+def test_sequences_of_one_token(dtype, D):
+    """They are decode steps, alone or beside longer and empty sequences, states in place or none."""
+    lengths = [1, 300, 0, 1, 1, 130]
+    cu = bounds(lengths)
+    x = inputs(cu, 3, D, dtype, 21, "cuda", states=True)
+    o, st = check_forward(x, cu, dtype)
+    kept = x["initial"].clone()
+    api.gated_prefill(*(x[n] for n in "qkvg"), cu_seqlens=cu, initial_state=kept, return_state=True, state_out=kept)
+    ok()
+    assert torch.equal(kept, st)
+    one = [s for s, n in enumerate(lengths) if n == 1]
+    rows = [cu[s] for s in one]
+    step = x["initial"][one].contiguous()
+    y = api.gated_decode_step(*(x[n][rows].contiguous() for n in "qkvg"), step)
+    ok()
+    assert torch.equal(y, o[rows]) and torch.equal(step, st[one])
+    fresh = {n: x[n] for n in "qkvg"}
+    check_forward(fresh, cu, dtype)
+    # only such and empty ones, packed and as a uniform batch
+    few = {n: x[n][:4].contiguous() for n in "qkvg"}
+    a, sa = check_forward(few, [0, 0, 1, 2, 2, 3, 4], dtype)
+    b, sb = api.gated_prefill(*(few[n].unsqueeze(1) for n in "qkvg"), return_state=True)
+    ok()
+    assert torch.equal(b.squeeze(1), a) and torch.equal(sb, sa[[1, 2, 4, 5]])
+
+
 # ------------------------------------------------------------------ backward
 @pytest.mark.parametrize("dtype,D", KINDS, ids=IDS)
 @pytest.mark.parametrize("lengths", LENGTHS.values(), ids=LENGTHS.keys())
