@@ -228,6 +228,8 @@ la_status la_gated_workspace(int B, int H, int N, int D, const int32_t *cu_seqle
  *   state_out [S][H][D][D] fp32 or NULL: the final states; may be state_in itself (update
  *             in place), but not overlap it otherwise.  A sequence of no tokens keeps its
  *             initial state.
+ * A sequence of one token is a decode step (the same bits as la_gated_decode_step), so that a
+ * packed call may mix requests that decode with chunks that prefill.
  */
 la_status la_gated_prefill(const void *q, const void *k, const void *v, const void *g, void *o,
                            int B, int H, int N, int D, const int32_t *cu_seqlens, int num_seqs,
