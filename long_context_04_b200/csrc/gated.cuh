@@ -92,6 +92,13 @@ struct GatedTable {
 // 2^14, whose rounding is 2^-10.  A NaN stays one.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.f : g; }
 
+// The kernels of one call overlap at their ends: each lets the next one's CTAs start as SMs
+// come free (next_may_start) and set up their shared memory and TMEM, which then wait for
+// all that the kernel before has written (previous_done) before they touch global memory.
+// (A backward call of 4096 tokens, 16 heads, D = 64: 73 us instead of 87.)
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // out = start states of a (sequence, head)'s segments from their own end states, in order:
 //     X_0 = initial, X_{s+1} = e^{total_s} X_s + local_s;   seg_state[s] <- X_s.
 // `rev` walks the segments from the last to the first (the state's gradient).  One thread
@@ -103,6 +110,8 @@ __global__ void __launch_bounds__(256)
                         const __grid_constant__ GatedTable tab) {
     const int rank = blockIdx.x / H, h = blockIdx.x % H;
     const int x = blockIdx.y * 256 + threadIdx.x;
+    next_may_start();
+    previous_done();
     int start, len, sid;
     tab.seqs.get(rank, start, len, sid);
     const int s0 = tab.first_seg(rank), ns = tab.num_segs(rank);

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(GatedPrefillCfg<D>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem_base;
+    previous_done();
     auto fail = [&]() {
         *abort_flag = 1;
         record_fault(DEV_TIMEOUT);

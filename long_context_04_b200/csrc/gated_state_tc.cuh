@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem_base;
+    next_may_start();
+    previous_done();
     auto fail = [&]() {
         *abort_flag = 1;
         record_fault(DEV_TIMEOUT);

@@ -292,6 +292,24 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
 
 la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
+// Launch; `behind`: a later kernel of the same call, whose CTAs may start before the kernel
+// before it has ended (they wait for its results themselves, see gated.cuh).
+template <typename... P, typename... A>
+la_status launch_behind(bool behind, void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                        const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
 // The sequences of one token of a prefill call.
 template <int D, typename E>
 la_status gated_rows(const void *q, const void *k, const void *v, const void *g, void *o, const float *state_in,
@@ -385,15 +403,14 @@ bool starts_with(K kern, int registers, std::atomic<bool> &known) {
 }
 
 template <int D, bool REV>
-la_status launch_gated_states(const la::GatedStateParams &p, cudaStream_t stream) {
+la_status launch_gated_states(const la::GatedStateParams &p, bool behind, cudaStream_t stream) {
     using C = la::GatedStateCfg<D, REV>;
     auto kern = la::gated_state_tc_kernel<D, REV>;
     static std::atomic<bool> fits{false};
     if (!starts_with(kern, C::R_LAUNCH, fits)) return LA_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
-    kern<<<(unsigned)(p.tab.segs * p.H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
-    return launched();
+    return launch_behind(behind, kern, dim3((unsigned)(p.tab.segs * p.H * C::NVS)), C::THREADS, C::SMEM_BYTES, stream, p);
 }
 
 template <int D>
@@ -410,20 +427,19 @@ bool fill_gated_states(la::GatedStateParams &p, const void *a, const void *b, co
 // The start states of a segmented call's segments (in place of their own end states).
 template <int D, bool REV>
 la_status gated_seg_states_tc(la::GatedStateParams p, const float *initial, const GatedPlan &pl, uint8_t *ws,
-                              cudaStream_t stream, float *&seg_in) {
+                              bool behind, cudaStream_t stream, float *&seg_in) {
     p.seg_out = seg_in = reinterpret_cast<float *>(ws + pl.seg_state);
     p.seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
-    if (la_status st = launch_gated_states<D, REV>(p, stream); st != LA_OK) return st;
-    la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * p.H), D * D / 1024), 256, 0, stream>>>(
-        reinterpret_cast<float4 *>(p.seg_out), p.seg_total, reinterpret_cast<const float4 *>(initial), p.H,
-        D * D / 4, REV ? 1 : 0, pl.tab);
-    return launched();
+    if (la_status st = launch_gated_states<D, REV>(p, behind, stream); st != LA_OK) return st;
+    return launch_behind(true, la::gated_prefix_kernel, dim3((unsigned)(pl.tab.S * p.H), D * D / 1024), 256, 0, stream,
+                         reinterpret_cast<float4 *>(p.seg_out), p.seg_total,
+                         reinterpret_cast<const float4 *>(initial), p.H, D * D / 4, REV ? 1 : 0, pl.tab);
 }
 
 template <int D, bool REV>
 la_status gated_states_tc(const void *a, const void *b, const void *g, const float *initial, void *snap,
                           const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
-                          uint8_t *ws, cudaStream_t stream) {
+                          uint8_t *ws, bool behind, cudaStream_t stream) {
     la::GatedStateParams p;
     const long long rows = (long long)pl.tab.blocks * H * D;
     if (!fill_gated_states<D>(p, a, b, g, H, T, pl) ||
@@ -432,14 +448,14 @@ la_status gated_states_tc(const void *a, const void *b, const void *g, const flo
         return LA_ERR_CUDA;
     if (pl.segmented) {
         float *seg_in = nullptr;
-        if (la_status st = gated_seg_states_tc<D, REV>(p, initial, pl, ws, stream, seg_in); st != LA_OK) return st;
+        if (la_status st = gated_seg_states_tc<D, REV>(p, initial, pl, ws, behind, stream, seg_in); st != LA_OK) return st;
         p.seg_in = seg_in;
     }
     p.initial = initial;
     p.fin = fin;
     p.have_snap = snap != nullptr;
     p.through = through;
-    return launch_gated_states<D, REV>(p, stream);
+    return launch_gated_states<D, REV>(p, behind || pl.segmented, stream);
 }
 
 // Final states of sequences without tokens: their initial states.
@@ -473,7 +489,8 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
         la::GatedStateParams sp;
         float *seg_in = nullptr;
         if (!fill_gated_states<D>(sp, k, v, g, H, T, pl)) return LA_ERR_CUDA;
-        if (la_status st = gated_seg_states_tc<D, false>(sp, state_in, pl, ws, stream, seg_in); st != LA_OK) return st;
+        if (la_status st = gated_seg_states_tc<D, false>(sp, state_in, pl, ws, false, stream, seg_in); st != LA_OK)
+            return st;
         p.seg_in = seg_in;
     }
     p.g = static_cast<const __nv_bfloat16 *>(g);
@@ -483,8 +500,8 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
     p.H = H;
     p.timeout_ns = kWaitLimitNs;
     p.tab = pl.tab;
-    kern<<<(unsigned)(pl.tab.segs * H * C::NVS), C::THREADS, C::SMEM_BYTES, stream>>>(p);
-    return launched();
+    return launch_behind(pl.segmented, kern, dim3((unsigned)(pl.tab.segs * H * C::NVS)), C::THREADS, C::SMEM_BYTES,
+                         stream, p);
 }
 
 template <int D>
@@ -501,12 +518,12 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
     if (snap != nullptr && dsnap != nullptr && dg != nullptr) through = reinterpret_cast<float *>(ws + pl.through);
     if (snap != nullptr)
         if (la_status st = gated_states_tc<D, false>(k, v, g, state_in, snap, nullptr, nullptr, nullptr, H, T, pl, ws,
-                                                     stream);
+                                                     false, stream);
             st != LA_OK)
             return st;
     if (dsnap != nullptr || d_state_in != nullptr)
         if (la_status st = gated_states_tc<D, true>(q, dout, g, d_state, dsnap, snap, through, d_state_in, H, T, pl,
-                                                    ws, stream);
+                                                    ws, snap != nullptr, stream);
             st != LA_OK)
             return st;
     la::GatedBackwardParams p;
@@ -531,8 +548,8 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
     auto kern = la::gated_backward_tc_kernel<D>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return LA_ERR_CUDA;
-    kern<<<(unsigned)std::min(kSMs, pl.tab.blocks * H), C::THREADS, C::SMEM_BYTES, stream>>>(p);
-    return launched();
+    return launch_behind(snap != nullptr || dsnap != nullptr || d_state_in != nullptr, kern,
+                         dim3((unsigned)std::min(kSMs, pl.tab.blocks * H)), C::THREADS, C::SMEM_BYTES, stream, p);
 }
 
 // Checks that the gated sequence operators share.
