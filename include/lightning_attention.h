@@ -263,8 +263,8 @@ la_status la_gated_prefill_backward(const void *q, const void *k, const void *v,
  *   slots      DEVICE array of B int32: the state of row b is slots[b].  -1 marks a padding
  *              row, of which nothing is read or written.  A slot outside the pool, and one
  *              that an earlier row of the call has, are skipped in the same way and reported
- *              as LA_ERR_DEVICE_RANGE by la_get_device_status.  NULL: row b has slot b (then
- *              B <= num_slots).
+ *              as LA_ERR_DEVICE_RANGE by la_get_device_status.  With slots B is at most
+ *              65536.  NULL: row b has slot b (then B <= num_slots).
  */
 la_status la_gated_decode_step(const void *q, const void *k, const void *v, const void *g,
                                float *state, void *o, int B, int H, int D, const int32_t *slots,

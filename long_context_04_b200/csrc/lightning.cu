@@ -167,6 +167,10 @@ la_status launch_simt(const float *q, const float *k, const float *v, float *o, 
 // ------------------------------------------------------------------ gated operators
 using la::GatedTable;
 
+// A row looks for its slot among the rows before it: at this many, 128 KB of them on average,
+// what the state of a row at D = 128 takes too.
+constexpr int LA_MAX_SLOT_ROWS = 65536;
+
 struct GatedPlan {
     GatedTable tab;
     bool segmented;
@@ -933,6 +937,7 @@ la_status la_gated_decode_step(const void *q, const void *k, const void *v, cons
         if (!aligned16(p)) return LA_ERR_INVALID_ARG;
     if (!aligned_gate(g, flags) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return LA_ERR_INVALID_ARG;
     if (slots == nullptr && num_slots < B) return LA_ERR_INVALID_ARG;
+    if (slots != nullptr && B > LA_MAX_SLOT_ROWS) return LA_ERR_UNSUPPORTED;
     if ((long long)B * H >= (1ll << 31)) return LA_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)(B * H);
     auto run = [&](auto *x) {

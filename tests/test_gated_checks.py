@@ -169,7 +169,7 @@ def test_workspace_sizes(L):
     (dict(H=0), api.LA_ERR_INVALID_ARG), (dict(D=32), api.LA_ERR_UNSUPPORTED),
     (dict(slots=None, pool=1), api.LA_ERR_INVALID_ARG), (dict(flags=3), api.LA_ERR_INVALID_ARG),
     (dict(pool=-1), api.LA_ERR_INVALID_ARG), (dict(B=1 << 20, H=1 << 12), api.LA_ERR_UNSUPPORTED),
-    (dict(B=0), api.LA_OK),
+    (dict(B=65537, H=1, pool=65537), api.LA_ERR_UNSUPPORTED), (dict(B=0), api.LA_OK),
 ])
 def test_decode_rejects(L, kw, code):
     a = dict(q=FAKE, g=FAKE, state=FAKE, B=2, H=2, D=128, slots=FAKE, pool=4, flags=1)
