@@ -504,7 +504,11 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
     p.H = H;
     p.timeout_ns = kWaitLimitNs;
     p.tab = pl.tab;
-    return launch_behind(pl.segmented, kern, dim3((unsigned)(pl.tab.segs * H * C::NVS)), C::THREADS, C::SMEM_BYTES,
+    // Started early, the two slices of a head land on SMs as these come free, not side by side,
+    // which slows a long pass by 1 %: 8 heads of 131072 tokens (114 blocks a segment) take 426 us
+    // and not 431 without; 4 heads of 32768 (15 blocks) 75 and not 78 with.
+    const bool behind = pl.segmented && pl.tab.seg_blocks <= 64;
+    return launch_behind(behind, kern, dim3((unsigned)(pl.tab.segs * H * C::NVS)), C::THREADS, C::SMEM_BYTES,
                          stream, p);
 }
 
