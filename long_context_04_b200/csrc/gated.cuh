@@ -103,10 +103,11 @@ __device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.w
 //     X_0 = initial, X_{s+1} = e^{total_s} X_s + local_s;   seg_state[s] <- X_s.
 // `rev` walks the segments from the last to the first (the state's gradient).  One thread
 // per float4 of the state; grid (S * H, D * D / 1024).  Latency-bound: eight segments' loads
-// are in flight at once.
+// are in flight at once.  `fin` (or nullptr) takes the state behind the last one; it may be
+// `initial`.
 __global__ void __launch_bounds__(256)
     gated_prefix_kernel(float4 *__restrict__ seg_state, const float *__restrict__ seg_total,
-                        const float4 *__restrict__ initial, int H, int n4, int rev,
+                        const float4 *initial, float4 *fin, int H, int n4, int rev,
                         const __grid_constant__ GatedTable tab) {
     const int rank = blockIdx.x / H, h = blockIdx.x % H;
     const int x = blockIdx.y * 256 + threadIdx.x;
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(256)
             X = make_float4(fmaf(w, X.x, l[e].x), fmaf(w, X.y, l[e].y), fmaf(w, X.z, l[e].z), fmaf(w, X.w, l[e].w));
         }
     }
+    if (fin != nullptr) fin[((size_t)sid * H + h) * n4 + x] = X;
 }
 
 // ------------------------------------------------------------------ CUDA-core kernels (fp32)

@@ -174,6 +174,7 @@ constexpr int LA_MAX_SLOT_ROWS = 65536;
 struct GatedPlan {
     GatedTable tab;
     bool segmented;
+    bool joined;                   // fp32: segments of one block, whose start states are the snapshots
     int longest;                   // blocks of the longest sequence
     // prefill: the sequences of one token, which are decode steps and not in the table (one
     // would hold a whole CTA per slice for one row)
@@ -253,6 +254,15 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         seg = lo;
     }
     pl.segmented = pl.longest > 2 * seg + 12;
+    // fp32: a block's snapshot is the start state of a segment of one block, so that with such
+    // segments the scan is one block long and joining them is all the rest.  Taken where the
+    // scan has SMs to spare (4 heads of 1000 tokens, D = 64, backward: 45 us and not 108; 64
+    // heads of 256, D = 128: 176 and not 159), the segments' own states, written and read once
+    // more, stay in L2, and joining (0.15 us a block) takes less than the chain (3 us a block;
+    // 1 head of 32768 tokens, D = 64: 243 us and not 184).
+    pl.joined = !tc && pl.longest >= 4 && S <= room && blocks * H * D * D * 4 <= (32ll << 20) &&
+                pl.longest + 20 < 20 * (pl.segmented ? 2 * seg + 3 : pl.longest);
+    if (pl.joined) pl.segmented = true, seg = 1;
     t.seg_blocks = pl.segmented ? (int)seg : std::max(1, pl.longest);
     long long nblk = 0, nseg = 0;
     if (t.seqs.varlen) {
@@ -285,10 +295,12 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         return o;
     };
     const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
-    pl.snap = take(tc && !backward ? 0 : (size_t)nblk * H * shot);
-    pl.dsnap = take(backward ? (size_t)nblk * H * shot : 0);
+    // (joined: the table has the sequences without blocks, which count as a segment, last)
+    const size_t shots = (size_t)(pl.joined ? nseg : nblk) * H * shot;
+    pl.snap = take(tc && !backward ? 0 : shots);
+    pl.dsnap = take(backward ? shots : 0);
     pl.through = take(tc && backward ? (size_t)nblk * H * 8 * slices * 4 : 0);
-    pl.seg_state = take(pl.segmented ? (size_t)nseg * H * state : 0);
+    pl.seg_state = take(pl.segmented && !pl.joined ? (size_t)nseg * H * state : 0);
     pl.seg_total = take(pl.segmented ? (size_t)nseg * H * 4 : 0);
     pl.bytes = at;
     return LA_OK;
@@ -335,15 +347,15 @@ la_status gated_states_simt(const float *a, const float *b, const float *g, cons
     const unsigned grid = (unsigned)(pl.tab.segs * H * (D / la::GatedSimt::VS));
     float *seg_state = nullptr, *seg_total = nullptr;
     if (pl.segmented) {
-        seg_state = reinterpret_cast<float *>(ws + pl.seg_state);
+        seg_state = pl.joined ? snap : reinterpret_cast<float *>(ws + pl.seg_state);
         seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
         kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
                                                          nullptr, nullptr, H, pl.tab);
         if (la_status st = launched(); st != LA_OK) return st;
         la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
-            reinterpret_cast<float4 *>(seg_state), seg_total, reinterpret_cast<const float4 *>(initial), H,
-            D * D / 4, REV ? 1 : 0, pl.tab);
-        if (la_status st = launched(); st != LA_OK) return st;
+            reinterpret_cast<float4 *>(seg_state), seg_total, reinterpret_cast<const float4 *>(initial),
+            pl.joined ? reinterpret_cast<float4 *>(fin) : nullptr, H, D * D / 4, REV ? 1 : 0, pl.tab);
+        if (la_status st = launched(); st != LA_OK || pl.joined) return st;
     }
     kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
                                                      H, pl.tab);
@@ -437,7 +449,7 @@ la_status gated_seg_states_tc(la::GatedStateParams p, const float *initial, cons
     if (la_status st = launch_gated_states<D, REV>(p, behind, stream); st != LA_OK) return st;
     return launch_behind(true, la::gated_prefix_kernel, dim3((unsigned)(pl.tab.S * p.H), D * D / 1024), 256, 0, stream,
                          reinterpret_cast<float4 *>(p.seg_out), p.seg_total,
-                         reinterpret_cast<const float4 *>(initial), p.H, D * D / 4, REV ? 1 : 0, pl.tab);
+                         reinterpret_cast<const float4 *>(initial), nullptr, p.H, D * D / 4, REV ? 1 : 0, pl.tab);
 }
 
 template <int D, bool REV>

@@ -253,6 +253,15 @@ def test_backward_uniform_batch_and_repeat(dtype):
         assert torch.equal(y, z.view(y.shape))
 
 
+@pytest.mark.parametrize("H,lengths", [(9, [3900, 0, 70]), (24, [1408, 1])], ids=["segments", "one chain"])
+def test_fp32_states_beyond_the_cache(H, lengths):
+    """fp32 calls whose blocks' states are too many to be formed block by block and joined."""
+    cu = bounds(lengths)
+    x = inputs(cu, H, 128, F32, 23, "cuda", grad=True, states=True)
+    check_forward(x, cu, F32)
+    check_backward(x, cu, F32)
+
+
 def test_gradient_against_differences():
     """The backward call against differences of the forward call's outputs (fp32)."""
     cu = bounds([75, 40])
