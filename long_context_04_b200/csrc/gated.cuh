@@ -95,6 +95,8 @@ __device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.
 // The kernels of one call overlap at their ends: each lets the next one's CTAs start as SMs
 // come free (next_may_start) and set up their shared memory and TMEM, which then wait for
 // all that the kernel before has written (previous_done) before they touch global memory.
+// What an earlier kernel of the call writes is no `const __restrict__` argument of a later
+// one: it changes while that one's CTAs already exist, and must not be read as constant.
 // (A backward call of 4096 tokens, 16 heads, D = 64: 73 us instead of 87.)
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -106,7 +108,7 @@ __device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.w
 // are in flight at once.  `fin` (or nullptr) takes the state behind the last one; it may be
 // `initial`.
 __global__ void __launch_bounds__(256)
-    gated_prefix_kernel(float4 *__restrict__ seg_state, const float *__restrict__ seg_total,
+    gated_prefix_kernel(float4 *seg_state, const float *seg_total,
                         const float4 *initial, float4 *fin, int H, int n4, int rev,
                         const __grid_constant__ GatedTable tab) {
     const int rank = blockIdx.x / H, h = blockIdx.x % H;
@@ -197,7 +199,7 @@ struct GatedStateSimt {
 template <int D, bool REV>
 __global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
     gated_state_simt_kernel(const float *__restrict__ a, const float *__restrict__ b, const float *__restrict__ g,
-                            const float *initial, const float *__restrict__ seg_in,
+                            const float *initial, const float *seg_in,
                             float *__restrict__ seg_out, float *__restrict__ seg_total,
                             float *__restrict__ snap, float *fin, int H,
                             const __grid_constant__ GatedTable tab) {
@@ -231,6 +233,8 @@ __global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
         cp_async_commit();
     };
     const bool adds = tid < GatedSimt::THREADS;  // the last warp: gate sums of the next block
+    next_may_start();
+    previous_done();
     auto sums = [&](int t) {
         const int blk = block_of(t);
         simt_gate_sums(sG[t & 1], g, start + blk * C, min(C, len - blk * C), H, h);
@@ -413,7 +417,7 @@ __device__ __forceinline__ void simt_rows_by_cols(float (&acc)[4][D / 16], const
 // contracted rows at a time through shared memory; the next slab is in registers meanwhile.
 template <int D, bool TM>
 __device__ __forceinline__ void simt_rows_by_state(float (&acc)[4][D / 16], const float *A,
-                                                   const float *__restrict__ M, float *slab) {
+                                                   const float *M, float *slab) {
     constexpr int LD = GatedSimtTiles<D>::LD, SR = GatedSimtTiles<D>::SROWS;
     constexpr int N = SR * D / 4 / GatedSimt::THREADS;
     const int tid = threadIdx.x;
@@ -463,7 +467,7 @@ __device__ __forceinline__ void simt_store_rows(float *__restrict__ dst, const f
 template <int D>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
     gated_prefill_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
-                              const float *__restrict__ g, float *__restrict__ o, const float *__restrict__ snap,
+                              const float *__restrict__ g, float *__restrict__ o, const float *snap,
                               int H, const __grid_constant__ GatedTable tab) {
     using L = GatedSimtTiles<D>;
     constexpr int C = GatedSimt::C;
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     tab.block(x, rank, blk);
     tab.seqs.get(rank, start, len, sid);
     const int row0 = start + blk * C, nv = min(C, len - blk * C);
+    previous_done();
     simt_load_tile<D>(sQ, q, row0, nv, H, h);
     simt_load_tile<D>(sK, k, row0, nv, H, h);
     simt_load_tile<D>(sV, v, row0, nv, H, h);
@@ -518,14 +523,14 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 
 // Gradients of one block of one head, from the state at its start (snap) and the state's
 // gradient at its end (dsnap); either may be nullptr for zero.  Bound by FMA issue and the
-// shared-memory loads that feed it; a call of 1000 tokens of 4 heads, D = 64, takes 113 us, of
-// which the two scans' chains of 16 blocks are the larger part.
+// shared-memory loads that feed it; a call of 1000 tokens of 4 heads, D = 64, takes 42 us, about
+// half of it here.
 template <int D>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
     gated_backward_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                                const float *__restrict__ g, const float *__restrict__ dout, float *__restrict__ dq,
                                float *__restrict__ dk, float *__restrict__ dv, float *__restrict__ dg,
-                               const float *__restrict__ snap, const float *__restrict__ dsnap, int H,
+                               const float *snap, const float *dsnap, int H,
                                const __grid_constant__ GatedTable tab) {
     using L = GatedSimtTiles<D>;
     constexpr int C = GatedSimt::C;
@@ -546,6 +551,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     const int row0 = start + blk * C, nv = min(C, len - blk * C);
     const float *S = snap != nullptr ? snap + ((size_t)x * H + h) * D * D : nullptr;
     const float *dS = dsnap != nullptr ? dsnap + ((size_t)x * H + h) * D * D : nullptr;
+    previous_done();
     simt_load_tile<D>(sQ, q, row0, nv, H, h);
     simt_load_tile<D>(sK, k, row0, nv, H, h);
     simt_load_tile<D>(sV, v, row0, nv, H, h);

@@ -339,7 +339,7 @@ la_status gated_rows(const void *q, const void *k, const void *v, const void *g,
 // State scan of one direction: snapshots per block, the final state where wanted.
 template <int D, bool REV>
 la_status gated_states_simt(const float *a, const float *b, const float *g, const float *initial, float *snap,
-                            float *fin, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
+                            float *fin, int H, const GatedPlan &pl, uint8_t *ws, bool behind, cudaStream_t stream) {
     auto kern = la::gated_state_simt_kernel<D, REV>;
     constexpr int smem = la::GatedStateSimt<D>::SMEM_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -349,17 +349,22 @@ la_status gated_states_simt(const float *a, const float *b, const float *g, cons
     if (pl.segmented) {
         seg_state = pl.joined ? snap : reinterpret_cast<float *>(ws + pl.seg_state);
         seg_total = reinterpret_cast<float *>(ws + pl.seg_total);
-        kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, nullptr, nullptr, seg_state, seg_total,
-                                                         nullptr, nullptr, H, pl.tab);
-        if (la_status st = launched(); st != LA_OK) return st;
-        la::gated_prefix_kernel<<<dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256, 0, stream>>>(
-            reinterpret_cast<float4 *>(seg_state), seg_total, reinterpret_cast<const float4 *>(initial),
-            pl.joined ? reinterpret_cast<float4 *>(fin) : nullptr, H, D * D / 4, REV ? 1 : 0, pl.tab);
-        if (la_status st = launched(); st != LA_OK || pl.joined) return st;
+        const float *none = nullptr;
+        if (la_status st = launch_behind(behind, kern, dim3(grid), la::GatedStateSimt<D>::THREADS, smem, stream, a, b, g,
+                                         none, none, seg_state, seg_total, nullptr, nullptr, H, pl.tab);
+            st != LA_OK)
+            return st;
+        la_status st = launch_behind(true, la::gated_prefix_kernel, dim3((unsigned)(pl.tab.S * H), D * D / 1024), 256,
+                                     0, stream, reinterpret_cast<float4 *>(seg_state), seg_total,
+                                     reinterpret_cast<const float4 *>(initial),
+                                     pl.joined ? reinterpret_cast<float4 *>(fin) : nullptr, H, D * D / 4, REV ? 1 : 0,
+                                     pl.tab);
+        if (st != LA_OK || pl.joined) return st;
     }
-    kern<<<grid, la::GatedStateSimt<D>::THREADS, smem, stream>>>(a, b, g, initial, seg_state, nullptr, nullptr, snap, fin,
-                                                     H, pl.tab);
-    return launched();
+    // (not behind the joining kernel: CTAs that start while SMs are still taken end up two to an
+    // SM beside idle ones; 32768 tokens of one head, D = 64, forward: 87 us, not 78)
+    return launch_behind(behind && !pl.segmented, kern, dim3(grid), la::GatedStateSimt<D>::THREADS, smem, stream, a, b, g,
+                         initial, seg_state, nullptr, nullptr, snap, fin, H, pl.tab);
 }
 
 template <int D>
@@ -369,7 +374,7 @@ la_status gated_prefill_simt(const float *q, const float *k, const float *v, con
     float *snap = nullptr;
     if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
     if (snap != nullptr || state_out != nullptr)
-        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, state_out, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, state_out, H, pl, ws, false, stream);
             st != LA_OK)
             return st;
     if (pl.tab.blocks == 0) return LA_OK;  // beside sequences of one token only empty ones
@@ -377,8 +382,8 @@ la_status gated_prefill_simt(const float *q, const float *k, const float *v, con
     constexpr int smem = la::GatedSimtTiles<D>::FWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
-    kern<<<(unsigned)(pl.tab.blocks * H), la::GatedSimt::THREADS, smem, stream>>>(q, k, v, g, o, snap, H, pl.tab);
-    return launched();
+    return launch_behind(snap != nullptr || state_out != nullptr, kern, dim3((unsigned)(pl.tab.blocks * H)),
+                         la::GatedSimt::THREADS, smem, stream, q, k, v, g, o, snap, H, pl.tab);
 }
 
 template <int D>
@@ -389,20 +394,21 @@ la_status gated_backward_simt(const float *q, const float *k, const float *v, co
     if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
     if (pl.longest > 1 || d_state != nullptr) dsnap = reinterpret_cast<float *>(ws + pl.dsnap);
     if (snap != nullptr)
-        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, false, stream);
             st != LA_OK)
             return st;
     if (dsnap != nullptr || d_state_in != nullptr)
-        if (la_status st = gated_states_simt<D, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, stream);
+        if (la_status st = gated_states_simt<D, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, snap != nullptr,
+                                                      stream);
             st != LA_OK)
             return st;
     auto kern = la::gated_backward_simt_kernel<D>;
     constexpr int smem = la::GatedSimtTiles<D>::BWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
-    kern<<<(unsigned)(pl.tab.blocks * H), la::GatedSimt::THREADS, smem, stream>>>(q, k, v, g, dout, dq, dk, dv, dg,
-                                                                                 snap, dsnap, H, pl.tab);
-    return launched();
+    return launch_behind(snap != nullptr || dsnap != nullptr || d_state_in != nullptr, kern,
+                         dim3((unsigned)(pl.tab.blocks * H)), la::GatedSimt::THREADS, smem, stream, q, k, v, g, dout, dq,
+                         dk, dv, dg, snap, dsnap, H, pl.tab);
 }
 
 // The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
