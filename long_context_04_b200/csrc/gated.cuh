@@ -151,15 +151,16 @@ struct GatedSimt {
 
 // Sums of the block's log-decays: sG[i] = g_0 + .. + g_i (i < nv; rows behind the sequence
 // repeat the last sum), in fp64, so that differences of two large sums stay exact to fp32.
-// Called by warp 0.
-__device__ __forceinline__ void simt_gate_sums(double *sG, const float *__restrict__ g, int row0, int nv,
+// Called by one warp.
+template <typename E>
+__device__ __forceinline__ void simt_gate_sums(double *sG, const E *__restrict__ g, int row0, int nv,
                                                int H, int h) {
     const int lane = threadIdx.x & 31;
     double carry = 0.0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = 32 * half + lane;
-        double x = i < nv && g != nullptr ? (double)clamp_gate(g[(size_t)(row0 + i) * H + h]) : 0.0;
+        double x = i < nv && g != nullptr ? (double)clamp_gate(to_f32(g[(size_t)(row0 + i) * H + h])) : 0.0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, x, off);
@@ -174,6 +175,20 @@ __device__ __forceinline__ void simt_gate_sums(double *sG, const float *__restri
 __device__ __forceinline__ void cp_async16(float *dst, const float *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
                  : "memory");
+}
+// Four elements to shared memory as fp32, zeros where `real` is not: fp32 by cp.async, bf16
+// through registers.
+__device__ __forceinline__ void simt_load4(float *dst, const float *src, bool real) { cp_async16(dst, src, real); }
+__device__ __forceinline__ void simt_load4(float *dst, const __nv_bfloat16 *src, bool real) {
+    const uint2 v = real ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
+    *reinterpret_cast<float4 *>(dst) = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                                   __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void simt_store4(float *dst, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(dst) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void simt_store4(__nv_bfloat16 *dst, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -196,9 +211,9 @@ struct GatedStateSimt {
     static constexpr int THREADS = GatedSimt::THREADS + 32;  // one warp forms the gate sums
 };
 
-template <int D, bool REV>
+template <int D, bool REV, typename E>
 __global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
-    gated_state_simt_kernel(const float *__restrict__ a, const float *__restrict__ b, const float *__restrict__ g,
+    gated_state_simt_kernel(const E *__restrict__ a, const E *__restrict__ b, const E *__restrict__ g,
                             const float *initial, const float *seg_in,
                             float *__restrict__ seg_out, float *__restrict__ seg_total,
                             float *__restrict__ snap, float *fin, int H,
@@ -223,12 +238,12 @@ __global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
 #pragma unroll
         for (int i = tid; i < C * D / 4; i += GatedSimt::THREADS) {
             const int rr = i / (D / 4), d = 4 * (i % (D / 4));
-            cp_async16(sa + rr * D + d, a + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + d, rr < nv);
+            simt_load4(sa + rr * D + d, a + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + d, rr < nv);
         }
 #pragma unroll
         for (int i = tid; i < C * VS / 4; i += GatedSimt::THREADS) {
             const int rr = i / (VS / 4), d = 4 * (i % (VS / 4));
-            cp_async16(sb + rr * VS + d, b + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + vs * VS + d, rr < nv);
+            simt_load4(sb + rr * VS + d, b + ((size_t)(row0 + min(rr, nv - 1)) * H + h) * D + vs * VS + d, rr < nv);
         }
         cp_async_commit();
     };
@@ -300,8 +315,9 @@ __global__ void __launch_bounds__(GatedStateSimt<D>::THREADS)
             X[r].z *= decay;
             X[r].w *= decay;
         }
+        const int seen = min(C, (len - blk * C + 7) & ~7);  // (rows behind the sequence are zeros)
 #pragma unroll 8
-        for (int c = 0; c < C; ++c) {
+        for (int c = 0; c < seen; ++c) {
             const float4 bb = *reinterpret_cast<const float4 *>(sb + c * VS + y0);
             float aa[R];
             if constexpr (R == 4)
@@ -342,23 +358,24 @@ struct GatedSimtTiles {
     static constexpr int BWD_BYTES = (4 * TILE + 2 * PT + ST) * 4 + GatedSimt::C * 8 + 6 * GatedSimt::C * 4 + 64;
 };
 
-// A tile by cp.async; rows behind the sequence are zeros.
-template <int D>
-__device__ __forceinline__ void simt_load_tile(float *dst, const float *__restrict__ src, int row0, int nv, int H,
+// A tile; rows behind the sequence are zeros.
+template <int D, typename E>
+__device__ __forceinline__ void simt_load_tile(float *dst, const E *__restrict__ src, int row0, int nv, int H,
                                                int h) {
     constexpr int LD = GatedSimtTiles<D>::LD;
 #pragma unroll
     for (int i = threadIdx.x; i < GatedSimt::C * D / 4; i += GatedSimt::THREADS) {
         const int r = i / (D / 4), d = 4 * (i % (D / 4));
-        cp_async16(dst + r * LD + d, src + ((size_t)(row0 + min(r, nv - 1)) * H + h) * D + d, r < nv);
+        simt_load4(dst + r * LD + d, src + ((size_t)(row0 + min(r, nv - 1)) * H + h) * D + d, r < nv);
     }
 }
 
 // acc[r][c] += sum_d A[4 ty + r][d] B[tx + 16 c][d]: the 64 x 64 products of two tiles' rows.
 template <int D>
-__device__ __forceinline__ void simt_rows_by_rows(float (&acc)[4][4], const float *A, const float *B) {
+__device__ __forceinline__ void simt_rows_by_rows(float (&acc)[4][4], const float *A, const float *B, int nv) {
     constexpr int LD = GatedSimtTiles<D>::LD;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (4 * ty >= nv) return;  // rows behind the sequence
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
@@ -379,12 +396,13 @@ __device__ __forceinline__ void simt_rows_by_rows(float (&acc)[4][4], const floa
 }
 
 // acc[r][4 g + e] += sum_{c < n} A(4 ty + r, c) B[c][64 g + 4 tx + e].  A(i, c) = A[i * la + c],
-// or A[c * la + i] with TA.
+// or A[c * la + i] with TA.  Rows i from nv on are left as they are.
 template <int D, bool TA>
 __device__ __forceinline__ void simt_rows_by_cols(float (&acc)[4][D / 16], const float *A, int la,
-                                                  const float *B, int n) {
+                                                  const float *B, int n, int nv) {
     constexpr int LD = GatedSimtTiles<D>::LD;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (4 * ty >= nv) return;
     for (int c0 = 0; c0 < n; c0 += 4) {
         float a[4][4];  // a[c][r]
 #pragma unroll
@@ -417,7 +435,7 @@ __device__ __forceinline__ void simt_rows_by_cols(float (&acc)[4][D / 16], const
 // contracted rows at a time through shared memory; the next slab is in registers meanwhile.
 template <int D, bool TM>
 __device__ __forceinline__ void simt_rows_by_state(float (&acc)[4][D / 16], const float *A,
-                                                   const float *M, float *slab) {
+                                                   const float *M, float *slab, int nv) {
     constexpr int LD = GatedSimtTiles<D>::LD, SR = GatedSimtTiles<D>::SROWS;
     constexpr int N = SR * D / 4 / GatedSimt::THREADS;
     const int tid = threadIdx.x;
@@ -446,12 +464,12 @@ __device__ __forceinline__ void simt_rows_by_state(float (&acc)[4][D / 16], cons
         }
         __syncthreads();
         if (c0 + SR < D) fetch(c0 + SR);
-        simt_rows_by_cols<D, false>(acc, A + c0, LD, slab, SR);
+        simt_rows_by_cols<D, false>(acc, A + c0, LD, slab, SR, nv);
     }
 }
 
-template <int D>
-__device__ __forceinline__ void simt_store_rows(float *__restrict__ dst, const float (&acc)[4][D / 16], int row0,
+template <int D, typename E>
+__device__ __forceinline__ void simt_store_rows(E *__restrict__ dst, const float (&acc)[4][D / 16], int row0,
                                                 int nv, int H, int h) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
@@ -459,8 +477,8 @@ __device__ __forceinline__ void simt_store_rows(float *__restrict__ dst, const f
         if (4 * ty + r < nv)
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
-                *reinterpret_cast<float4 *>(dst + ((size_t)(row0 + 4 * ty + r) * H + h) * D + 64 * x + 4 * tx) =
-                    make_float4(acc[r][4 * x], acc[r][4 * x + 1], acc[r][4 * x + 2], acc[r][4 * x + 3]);
+                simt_store4(dst + ((size_t)(row0 + 4 * ty + r) * H + h) * D + 64 * x + 4 * tx, acc[r][4 * x],
+                            acc[r][4 * x + 1], acc[r][4 * x + 2], acc[r][4 * x + 3]);
 }
 
 // Output of one block of one head, from the state at its start (snap; nullptr: zero).
@@ -490,7 +508,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     __syncthreads();
     {
         float p[4][4] = {};
-        simt_rows_by_rows<D>(p, sQ, sK);
+        simt_rows_by_rows<D>(p, sQ, sK, C);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     }
     float acc[4][D / 16] = {};
     if (snap != nullptr) {
-        simt_rows_by_state<D, false>(acc, sQ, snap + ((size_t)x * H + h) * D * D, slab);
+        simt_rows_by_state<D, false>(acc, sQ, snap + ((size_t)x * H + h) * D * D, slab, C);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const float w = expf((float)sG[4 * ty + r]);
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         }
     }
     __syncthreads();
-    simt_rows_by_cols<D, false>(acc, sP, L::LP, sV, C);
+    simt_rows_by_cols<D, false>(acc, sP, L::LP, sV, C, C);
     simt_store_rows<D>(o, acc, row0, nv, H, h);
 }
 
@@ -524,13 +542,14 @@ __device__ __forceinline__ float half_warp_sum(float x) {
 // Gradients of one block of one head, from the state at its start (snap) and the state's
 // gradient at its end (dsnap); either may be nullptr for zero.  Bound by FMA issue and the
 // shared-memory loads that feed it; a call of 1000 tokens of 4 heads, D = 64, takes 42 us, about
-// half of it here.
-template <int D>
+// half of it here.  `by_seq`: sequences of one block, whose states are the call's own (indexed
+// by sequence, not by block).
+template <int D, typename E>
 __global__ void __launch_bounds__(GatedSimt::THREADS)
-    gated_backward_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
-                               const float *__restrict__ g, const float *__restrict__ dout, float *__restrict__ dq,
-                               float *__restrict__ dk, float *__restrict__ dv, float *__restrict__ dg,
-                               const float *snap, const float *dsnap, int H,
+    gated_backward_simt_kernel(const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v,
+                               const E *__restrict__ g, const E *__restrict__ dout, E *__restrict__ dq,
+                               E *__restrict__ dk, E *__restrict__ dv, E *__restrict__ dg,
+                               const float *snap, const float *dsnap, int by_seq, int H,
                                const __grid_constant__ GatedTable tab) {
     using L = GatedSimtTiles<D>;
     constexpr int C = GatedSimt::C;
@@ -549,8 +568,8 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     tab.block(x, rank, blk);
     tab.seqs.get(rank, start, len, sid);
     const int row0 = start + blk * C, nv = min(C, len - blk * C);
-    const float *S = snap != nullptr ? snap + ((size_t)x * H + h) * D * D : nullptr;
-    const float *dS = dsnap != nullptr ? dsnap + ((size_t)x * H + h) * D * D : nullptr;
+    const size_t at = ((size_t)(by_seq ? sid : x) * H + h) * D * D;
+    const float *S = snap != nullptr ? snap + at : nullptr, *dS = dsnap != nullptr ? dsnap + at : nullptr;
     previous_done();
     simt_load_tile<D>(sQ, q, row0, nv, H, h);
     simt_load_tile<D>(sK, k, row0, nv, H, h);
@@ -568,8 +587,8 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     }
     {
         float p[4][4] = {}, dp[4][4] = {};
-        simt_rows_by_rows<D>(p, sQ, sK);
-        simt_rows_by_rows<D>(dp, sO, sV);
+        simt_rows_by_rows<D>(p, sQ, sK, nv);
+        simt_rows_by_rows<D>(dp, sO, sV, nv);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             float row = 0.f;
@@ -598,7 +617,7 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
     }
     // dq = dP k + e^{G_i} S do_i
     float acc[4][D / 16] = {};
-    if (S != nullptr) simt_rows_by_state<D, true>(acc, sO, S, slab);
+    if (S != nullptr) simt_rows_by_state<D, true>(acc, sO, S, slab, nv);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         float s = 0.f;
@@ -611,14 +630,14 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         if (tx == 0) sR[4 * ty + r] = s;
     }
     __syncthreads();
-    simt_rows_by_cols<D, false>(acc, sdP, L::LP, sK, C);
+    simt_rows_by_cols<D, false>(acc, sdP, L::LP, sK, (nv + 3) & ~3, nv);
     simt_store_rows<D>(dq, acc, row0, nv, H, h);
     // dk = dP^T q + e^{G_C - G_j} dS v_j
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) acc[r][e] = 0.f;
-    if (dS != nullptr) simt_rows_by_state<D, true>(acc, sV, dS, slab);
+    if (dS != nullptr) simt_rows_by_state<D, true>(acc, sV, dS, slab, nv);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         float s = 0.f;
@@ -630,19 +649,19 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         s = half_warp_sum(s);
         if (tx == 0) sE[4 * ty + r] = s;
     }
-    simt_rows_by_cols<D, true>(acc, sdP, L::LP, sQ, C);
+    simt_rows_by_cols<D, true>(acc, sdP, L::LP, sQ, (nv + 3) & ~3, nv);
     simt_store_rows<D>(dk, acc, row0, nv, H, h);
     // dv = P^T do + e^{G_C - G_j} dS^T k_j
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) acc[r][e] = 0.f;
-    if (dS != nullptr) simt_rows_by_state<D, false>(acc, sK, dS, slab);
+    if (dS != nullptr) simt_rows_by_state<D, false>(acc, sK, dS, slab, nv);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) acc[r][e] *= wcol[r];
-    simt_rows_by_cols<D, true>(acc, sP, L::LP, sO, C);
+    simt_rows_by_cols<D, true>(acc, sP, L::LP, sO, (nv + 3) & ~3, nv);
     simt_store_rows<D>(dv, acc, row0, nv, H, h);
     // <dS, S>
     float f = 0.f;
@@ -674,8 +693,8 @@ __global__ void __launch_bounds__(GatedSimt::THREADS)
         if (tid == 0) before = 0.f;
         float after = __shfl_down_sync(0xffffffffu, up, 1);   // sum_{i >= t0 + 2}
         if (tid == 31) after = 0.f;
-        if (t0 < nv) dg[(size_t)(row0 + t0) * H + h] = through + up + before;
-        if (t0 + 1 < nv) dg[(size_t)(row0 + t0 + 1) * H + h] = through + after + r1 + before + e0;
+        if (t0 < nv) dg[(size_t)(row0 + t0) * H + h] = from_f32<E>(through + up + before);
+        if (t0 + 1 < nv) dg[(size_t)(row0 + t0 + 1) * H + h] = from_f32<E>(through + after + r1 + before + e0);
     }
 }
 

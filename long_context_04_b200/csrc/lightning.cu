@@ -174,6 +174,7 @@ constexpr int LA_MAX_SLOT_ROWS = 65536;
 struct GatedPlan {
     GatedTable tab;
     bool segmented;
+    bool simt;                     // on the CUDA cores: fp32, and backward passes of short sequences
     bool joined;                   // fp32: segments of one block, whose start states are the snapshots
     int longest;                   // blocks of the longest sequence
     // prefill: the sequences of one token, which are decode steps and not in the table (one
@@ -184,6 +185,8 @@ struct GatedPlan {
     // segment states, their decays
     size_t snap, dsnap, through, seg_state, seg_total, bytes;
 };
+
+constexpr int kShortTokens = 16, kShortRows = 2 * kSMs;
 
 // The table and the workspace of a call.  A state scan runs one CTA per (segment, head,
 // slice), one block after the other.  Cutting sequences into segments shortens the longest
@@ -199,7 +202,14 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
     // tensor cores: 128-token blocks, bf16 snapshots (of the backward pass alone: the prefill
     // kernel keeps its state on chip); CUDA cores: 64-token blocks, fp32 snapshots
-    const bool tc = (flags & LA_BF16) != 0;
+    // The backward pass of a few short sequences runs on the CUDA cores whatever the type, with
+    // scores and states in fp32: over few tokens their bf16 roundings do not average out (up to
+    // 3.8 times the rounding of the result were seen).  It is one or two kernels instead of three:
+    // 64 heads, 16 tokens take 19 us and not 21 at D = 64, 13 us and not 12 (with states 37 and
+    // not 27) at D = 128; from 300 (sequence, head) pairs on it takes longer.
+    const int most = t.seqs.varlen ? (S > 0 ? t.seqs.seq_len[0] : 0) : N;
+    pl.simt = (flags & LA_BF16) == 0 || (backward && most <= kShortTokens && (long long)S * H <= kShortRows);
+    const bool tc = !pl.simt;
     const int C = tc ? 128 : la::GatedSimt::C, slices = tc ? D / 64 : D / la::GatedSimt::VS;
     const int resident = kSMs, min_seg = 4;
     pl.ones = pl.one.identity = 0;
@@ -296,7 +306,8 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     };
     const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
     // (joined: the table has the sequences without blocks, which count as a segment, last)
-    const size_t shots = (size_t)(pl.joined ? nseg : nblk) * H * shot;
+    const bool own = !tc && backward && pl.longest <= 1;  // the call's own states serve
+    const size_t shots = own ? 0 : (size_t)(pl.joined ? nseg : nblk) * H * shot;
     pl.snap = take(tc && !backward ? 0 : shots);
     pl.dsnap = take(backward ? shots : 0);
     pl.through = take(tc && backward ? (size_t)nblk * H * 8 * slices * 4 : 0);
@@ -337,10 +348,10 @@ la_status gated_rows(const void *q, const void *k, const void *v, const void *g,
 }
 
 // State scan of one direction: snapshots per block, the final state where wanted.
-template <int D, bool REV>
-la_status gated_states_simt(const float *a, const float *b, const float *g, const float *initial, float *snap,
+template <int D, bool REV, typename E>
+la_status gated_states_simt(const E *a, const E *b, const E *g, const float *initial, float *snap,
                             float *fin, int H, const GatedPlan &pl, uint8_t *ws, bool behind, cudaStream_t stream) {
-    auto kern = la::gated_state_simt_kernel<D, REV>;
+    auto kern = la::gated_state_simt_kernel<D, REV, E>;
     constexpr int smem = la::GatedStateSimt<D>::SMEM_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
@@ -386,29 +397,37 @@ la_status gated_prefill_simt(const float *q, const float *k, const float *v, con
                          la::GatedSimt::THREADS, smem, stream, q, k, v, g, o, snap, H, pl.tab);
 }
 
-template <int D>
-la_status gated_backward_simt(const float *q, const float *k, const float *v, const float *g, const float *dout,
-                              float *dq, float *dk, float *dv, float *dg, const float *state_in, const float *d_state,
+template <int D, typename E>
+la_status gated_backward_simt(const void *q_, const void *k_, const void *v_, const void *g_, const void *dout_, void *dq,
+                              void *dk, void *dv, void *dg, const float *state_in, const float *d_state,
                               float *d_state_in, int H, const GatedPlan &pl, uint8_t *ws, cudaStream_t stream) {
-    float *snap = nullptr, *dsnap = nullptr;
-    if (pl.longest > 1 || state_in != nullptr) snap = reinterpret_cast<float *>(ws + pl.snap);
-    if (pl.longest > 1 || d_state != nullptr) dsnap = reinterpret_cast<float *>(ws + pl.dsnap);
-    if (snap != nullptr)
-        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, false, stream);
-            st != LA_OK)
-            return st;
-    if (dsnap != nullptr || d_state_in != nullptr)
-        if (la_status st = gated_states_simt<D, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, snap != nullptr,
-                                                      stream);
-            st != LA_OK)
-            return st;
-    auto kern = la::gated_backward_simt_kernel<D>;
+    const E *q = static_cast<const E *>(q_), *k = static_cast<const E *>(k_), *v = static_cast<const E *>(v_),
+            *g = static_cast<const E *>(g_), *dout = static_cast<const E *>(dout_);
+    auto kern = la::gated_backward_simt_kernel<D, E>;
     constexpr int smem = la::GatedSimtTiles<D>::BWD_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LA_ERR_CUDA;
-    return launch_behind(snap != nullptr || dsnap != nullptr || d_state_in != nullptr, kern,
-                         dim3((unsigned)(pl.tab.blocks * H)), la::GatedSimt::THREADS, smem, stream, q, k, v, g, dout, dq,
-                         dk, dv, dg, snap, dsnap, H, pl.tab);
+    auto blocks = [&](bool behind, const float *snap, const float *dsnap, int by_seq) {
+        return launch_behind(behind, kern, dim3((unsigned)(pl.tab.blocks * H)), la::GatedSimt::THREADS, smem, stream, q,
+                             k, v, g, dout, static_cast<E *>(dq), static_cast<E *>(dk), static_cast<E *>(dv),
+                             static_cast<E *>(dg), snap, dsnap, by_seq, H, pl.tab);
+    };
+    if (pl.longest <= 1) {
+        // no block but the first: its states are the call's.  (d_state_in may be d_state: last.)
+        if (la_status st = blocks(false, state_in, d_state, 1); st != LA_OK || d_state_in == nullptr) return st;
+        return gated_states_simt<D, true>(q, dout, g, d_state, nullptr, d_state_in, H, pl, ws, true, stream);
+    }
+    float *snap = reinterpret_cast<float *>(ws + pl.snap), *dsnap = reinterpret_cast<float *>(ws + pl.dsnap);
+    if constexpr (std::is_same_v<E, float>) {
+        if (la_status st = gated_states_simt<D, false>(k, v, g, state_in, snap, nullptr, H, pl, ws, false, stream);
+            st != LA_OK)
+            return st;
+        if (la_status st = gated_states_simt<D, true>(q, dout, g, d_state, dsnap, d_state_in, H, pl, ws, true, stream);
+            st != LA_OK)
+            return st;
+        return blocks(true, snap, dsnap, 0);
+    }
+    return LA_ERR_UNSUPPORTED;  // bf16 comes here with single blocks alone
 }
 
 // The tensor-core state scan of one direction (bf16): a = k, b = v, or reversed a = q, b = do.
@@ -927,23 +946,17 @@ la_status la_gated_prefill_backward(const void *q, const void *k, const void *v,
     if (pl.bytes > workspace_bytes || (pl.bytes > 0 && workspace == nullptr)) return LA_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (T == 0) return gated_no_tokens(d_state, d_state_in, pl.tab.S, H, D, stream);
-    if (flags & LA_BF16) {
-        if (D == 128)
-            return gated_backward_tc<128>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
-                                          stream);
-        return gated_backward_tc<64>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
-                                     stream);
-    }
-    const float *qf = static_cast<const float *>(q), *kf = static_cast<const float *>(k),
-                *vf = static_cast<const float *>(v), *gf = static_cast<const float *>(g),
-                *df = static_cast<const float *>(dout);
-    float *dqf = static_cast<float *>(dq), *dkf = static_cast<float *>(dk), *dvf = static_cast<float *>(dv),
-          *dgf = static_cast<float *>(dg);
+    auto *run = pl.simt ? ((flags & LA_BF16) ? (D == 128 ? gated_backward_simt<128, __nv_bfloat16>
+                                                         : gated_backward_simt<64, __nv_bfloat16>)
+                                             : (D == 128 ? gated_backward_simt<128, float>
+                                                         : gated_backward_simt<64, float>))
+                        : nullptr;
+    if (run != nullptr)
+        return run(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, pl, ws, stream);
     if (D == 128)
-        return gated_backward_simt<128>(qf, kf, vf, gf, df, dqf, dkf, dvf, dgf, state_in, d_state, d_state_in, H, pl, ws,
-                                        stream);
-    return gated_backward_simt<64>(qf, kf, vf, gf, df, dqf, dkf, dvf, dgf, state_in, d_state, d_state_in, H, pl, ws,
-                                   stream);
+        return gated_backward_tc<128>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws,
+                                      stream);
+    return gated_backward_tc<64>(q, k, v, g, dout, dq, dk, dv, dg, state_in, d_state, d_state_in, H, T, pl, ws, stream);
 }
 
 la_status la_gated_decode_step(const void *q, const void *k, const void *v, const void *g, float *state, void *o,

@@ -10,6 +10,8 @@ itself; the fp32 path rounds by 2^-24.
   fp32 results and states: sums of up to a few thousand fp32 terms, each added with an error
       of 2^-24 of the running sum: below 1e-5 as for the ungated operators.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -251,6 +253,30 @@ def test_backward_uniform_batch_and_repeat(dtype):
     ok()
     for y, z in zip(got, again):
         assert torch.equal(y, z.view(y.shape))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("H,lengths", [(2, [9, 0, 1, 16]), (2, [40, 3]), (2, [700, 9]), (80, [5, 0, 16, 2])])
+def test_backward_state_gradient_in_place(dtype, H, lengths):
+    """The gradient of the initial states written over that of the final ones, at the C boundary;
+    calls of short sequences, of single blocks and of several."""
+    cu = bounds(lengths)
+    x = inputs(cu, H, 64, dtype, 24, "cuda", grad=True, states=True)
+    want = check_backward(x, cu, dtype)
+    flags = api.LA_BF16 if dtype == BF else api.LA_FP32
+    c = np.asarray(cu, np.int32)
+    n = ctypes.c_ulonglong()
+    L = api.lib()
+    assert L.la_gated_workspace(1, H, cu[-1], 64, c.ctypes.data, len(lengths), flags, 1, ctypes.byref(n)) == api.LA_OK
+    ws = torch.full((max(n.value, 16),), 255, dtype=torch.uint8, device="cuda")
+    got = [torch.full_like(t, float("nan")) for t in want[:4]] + [x["d_state"].clone()]
+    ptr = [t.data_ptr() for t in got]
+    rc = L.la_gated_prefill_backward(*(x[k].data_ptr() for k in ("q", "k", "v", "g", "do")), *ptr[:4], 1, H, cu[-1], 64,
+                                     c.ctypes.data, len(lengths), flags, x["initial"].data_ptr(), ptr[4], ptr[4],
+                                     ws.data_ptr(), n.value, torch.cuda.current_stream().cuda_stream)
+    assert rc == api.LA_OK
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @pytest.mark.parametrize("H,lengths", [(9, [3900, 0, 70]), (24, [1408, 1])], ids=["segments", "one chain"])
