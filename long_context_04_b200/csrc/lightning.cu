@@ -269,8 +269,10 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     // scan has SMs to spare (4 heads of 1000 tokens, D = 64, backward: 45 us and not 108; 64
     // heads of 256, D = 128: 176 and not 159), the segments' own states, written and read once
     // more, stay in L2, and joining (0.15 us a block) takes less than the chain (3 us a block;
-    // 1 head of 32768 tokens, D = 64: 243 us and not 184).
-    pl.joined = !tc && pl.longest >= 4 && S <= room && blocks * H * D * D * 4 <= (32ll << 20) &&
+    // 1 head of 32768 tokens, D = 64: 243 us and not 184).  A forward call of fewer than eight
+    // blocks would wait for the host's third launch instead (2 heads of 256: 16 us of GPU time
+    // and not 22, but 31 and not 25 from call to call).
+    pl.joined = !tc && pl.longest >= (backward ? 4 : 8) && S <= room && blocks * H * D * D * 4 <= (32ll << 20) &&
                 pl.longest + 20 < 20 * (pl.segmented ? 2 * seg + 3 : pl.longest);
     if (pl.joined) pl.segmented = true, seg = 1;
     t.seg_blocks = pl.segmented ? (int)seg : std::max(1, pl.longest);
@@ -321,9 +323,13 @@ la_status launched() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR
 
 // Launch; `behind`: a later kernel of the same call, whose CTAs may start before the kernel
 // before it has ended (they wait for its results themselves, see gated.cuh).
-template <typename... P, typename... A>
+template <typename T>
+struct as_given {
+    using type = T;
+};
+template <typename... P>
 la_status launch_behind(bool behind, void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                        const A &...args) {
+                        const typename as_given<P>::type &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -334,7 +340,9 @@ la_status launch_behind(bool behind, void (*kern)(P...), dim3 grid, int threads,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = behind ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    // (by address: the tables are 20 KB)
+    void *at[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kern), at) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 // The sequences of one token of a prefill call.
