@@ -554,6 +554,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                     sE[i] = e;
                     tmem_st_wait();
                     tc_fence_before();
+                    // the products that wait for this arrival let TMA take the places of q and k,
+                    // whose rows were read above
+                    fence_proxy_async_smem();
                     mbar_arrive(&m->scaled);
                     ok = wwait(&m->dq_full, ph);
                 }

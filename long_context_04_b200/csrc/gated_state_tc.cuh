@@ -357,8 +357,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return r;
 }
 // What this thread has read from shared memory so far has been read: behind it an arrival may
-// give the place away.  The arrival alone does not see to that: loads were found to take
-// place behind it, after the place had been refilled.
+// give the place to other threads' ordinary stores.  (An arrival releases ordinary accesses of
+// its own thread; where lane 0 arrives for its warp, the others' reads come before it through
+// this and __syncwarp.)  A place that TMA or a product's operands take next needs
+// fence_proxy_async_smem instead: the barrier does not order ordinary reads with the async
+// proxy's writes, and rows were seen to be loaded after their place had been refilled.
 __device__ __forceinline__ void reads_done() { __threadfence_block(); }
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4 &v) {
     st_shared_v4(addr, v.x, v.y, v.z, v.w);
