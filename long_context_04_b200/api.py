@@ -5,6 +5,11 @@ tensors of the expected dtype, and passes their data pointers, sizes and the
 current CUDA stream to the C entry point of the same name.  Every step of the
 computation runs in the library's kernels; there is no Python or CPU path, and
 a missing or unloadable library raises ``LightningLibraryError``.
+
+With ``stream=`` the kernels run on that stream.  The caller orders it behind the work that
+makes the arguments, and what reads the results behind it.  Memory needs no care: results and
+workspaces come from that stream's pool, and a tensor may be freed on either stream as soon as
+the call has returned.
 """
 from __future__ import annotations
 
@@ -103,6 +108,35 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+def _aside(dev, stream):
+    """The current stream, where ``stream`` is another one; else None."""
+    if stream is None:
+        return None
+    here = torch.cuda.current_stream(dev)
+    return None if stream == here else here
+
+
+def _new(make, stream, here):
+    """``make()``, a tensor that a call on ``stream`` writes.  It comes from that stream's pool: the
+    block of a tensor freed on the current stream may still be in use there when the kernels on
+    ``stream`` write it.  The current stream, where the caller reads it, is recorded."""
+    if here is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
+def _keep(stream, here, *tensors):
+    """Arguments of a call on ``stream``: freed on the current stream, their memory is not given
+    out before the call has run."""
+    if here is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _on_gpu(t: torch.Tensor) -> bool:
     return t.is_cuda
 
@@ -199,13 +233,14 @@ def prefill(q, k, v, *, beta: int = 128, cu_seqlens=None, rmsnorm: bool = False,
     cu = None
     if cu_seqlens is not None:
         cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    here = _aside(dev, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(lambda: torch.empty_like(q), stream, here)
     _need(out, "out", q.dtype, dev)
     _need_shape(out, "out", q.shape)
     st = state_out
     if return_state and st is None:
-        st = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
+        st = _new(lambda: torch.empty((S, H, D, D), dtype=torch.float32, device=dev), stream, here)
     if st is not None:
         _need(st, "state_out", torch.float32, dev)
         _need_shape(st, "state_out", (S, H, D, D))
@@ -228,6 +263,7 @@ def prefill(q, k, v, *, beta: int = 128, cu_seqlens=None, rmsnorm: bool = False,
     if rmsnorm:
         flags |= LA_OUT_RMSNORM
     cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    _keep(stream, here, q, k, v, initial_state, out, state_out)
     with _on_device(dev, stream):
         if copy_in:
             _copy_state(initial_state, st, stream)   # the library's copy kernel
@@ -264,10 +300,12 @@ def decode_step(q, k, v, state, *, rmsnorm: bool = False, out=None, stream=None)
     if tuple(state.shape) != (B, H, D, D):
         raise ValueError("state must be [B, H, D, D]")
     flags = _flags_for(q.dtype) | (LA_OUT_RMSNORM if rmsnorm else 0)
+    here = _aside(dev, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(lambda: torch.empty_like(q), stream, here)
     _need(out, "out", q.dtype, dev)
     _need_shape(out, "out", q.shape)
+    _keep(stream, here, q, k, v, state, out)
     with _on_device(dev, stream):
         rc = lib().la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(state), _ptr(out), B, H, D,
                                   flags, _stream_ptr(stream))
@@ -289,6 +327,7 @@ def state_out(state_ws, state_dst, seq_to_slot=None, *, stream=None):
     if seq_to_slot is not None:
         _need(seq_to_slot, "seq_to_slot", torch.int32, dev)
         _need_shape(seq_to_slot, "seq_to_slot", (S,))
+    _keep(stream, _aside(dev, stream), state_ws, state_dst, seq_to_slot)
     with _on_device(dev, stream):
         rc = lib().la_state_out(_ptr(state_ws), _ptr(state_dst), S, H, D, _ptr(seq_to_slot),
                                 state_dst.shape[0], _stream_ptr(stream))
@@ -317,11 +356,13 @@ def chunk_state(k, v, *, cu_seqlens=None, state_out=None, stream=None):
     else:
         raise ValueError("k must be [B, N, H, D] or [T, H, D]")
     cu = None if cu_seqlens is None else np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    here = _aside(dev, stream)
     if state_out is None:
-        state_out = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
+        state_out = _new(lambda: torch.empty((S, H, D, D), dtype=torch.float32, device=dev), stream, here)
     _need(state_out, "state_out", torch.float32, dev)
     _need_shape(state_out, "state_out", (S, H, D, D))
     cu_ptr = None if cu is None else cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    _keep(stream, here, k, v, state_out)
     with _on_device(dev, stream):
         rc = lib().la_chunk_state(_ptr(k), _ptr(v), B, H, N, D, cu_ptr,
                                   0 if cu is None else len(cu) - 1, flags, _ptr(state_out),
@@ -338,12 +379,14 @@ def state_prefix(gathered, rank: int, *, out=None, stream=None):
     if gathered.dim() != 5:
         raise ValueError("gathered must be [R, S, H, D, D]")
     R, S, H, D, _ = gathered.shape
+    here = _aside(dev, stream)
     if out is None:
-        out = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
+        out = _new(lambda: torch.empty((S, H, D, D), dtype=torch.float32, device=dev), stream, here)
     _need(out, "out", torch.float32, dev)
     _need_shape(out, "out", (S, H, D, D))
     if _overlap(gathered, out):
         raise ValueError("out must not overlap gathered")
+    _keep(stream, here, gathered, out)
     with _on_device(dev, stream):
         rc = lib().la_state_prefix(_ptr(gathered), R, int(rank), S, H, D, _ptr(out),
                                    _stream_ptr(stream))
@@ -425,14 +468,6 @@ def _gated_workspace(args, cu_ptr, num_seqs, flags, backward, dev, stream):
         return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
 
 
-def _used_on(stream, *tensors):
-    """Outputs allocated here on the current stream and written on ``stream``."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, state_out=None,
                   out=None, initial_state=None, stream=None):
     """Causal lightning attention whose state decays: ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``,
@@ -446,10 +481,9 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
     """
     (B, H, N, D, S), (cu, cu_ptr, num_seqs) = _gated_shape(q, k, v, g, cu_seqlens)
     dev, flags = q.device, _flags_for(q.dtype)
-    made = []
+    here = _aside(dev, stream)
     if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
+        out = _new(lambda: torch.empty_like(q), stream, here)
     else:
         _need(out, "out", q.dtype, dev)
         _need_shape(out, "out", q.shape)
@@ -457,8 +491,7 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
             raise ValueError("out must not overlap an input")
     st = state_out
     if return_state and st is None:
-        st = torch.empty((S, H, D, D), dtype=torch.float32, device=dev)
-        made.append(st)
+        st = _new(lambda: torch.empty((S, H, D, D), dtype=torch.float32, device=dev), stream, here)
     _need_state(state_out, "state_out", (S, H, D, D), dev)
     _need_state(initial_state, "initial_state", (S, H, D, D), dev)
     if state_out is not None:
@@ -467,9 +500,9 @@ def gated_prefill(q, k, v, g, *, cu_seqlens=None, return_state: bool = False, st
         if any(_overlap(st, t) for t in (q, k, v, g, out) if t is not None):
             raise ValueError("state_out must not overlap an input or out")
     ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 0, dev, stream)
+    _keep(stream, here, q, k, v, g, initial_state, out, state_out)
     _call("la_gated_prefill", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(out), B, H, N, D, cu_ptr,
           num_seqs, flags, _ptr(initial_state), _ptr(st), _ptr(ws), size)
-    _used_on(stream, *made)
     return (out, st) if st is not None else out
 
 
@@ -488,14 +521,14 @@ def gated_prefill_backward(q, k, v, g, do, *, cu_seqlens=None, initial_state=Non
     _need_shape(do, "do", q.shape)
     _need_state(initial_state, "initial_state", (S, H, D, D), dev)
     _need_state(d_state, "d_state", (S, H, D, D), dev)
-    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
-    dg = None if g is None else torch.empty_like(g)
-    d_init = None if initial_state is None else torch.empty_like(initial_state)
+    here = _aside(dev, stream)
+    dq, dk, dv, dg, d_init = (None if t is None else _new(lambda t=t: torch.empty_like(t), stream, here)
+                              for t in (q, q, q, g, initial_state))
     ws, size = _gated_workspace((B, H, N, D), cu_ptr, num_seqs, flags, 1, dev, stream)
+    _keep(stream, here, q, k, v, g, do, initial_state, d_state)
     _call("la_gated_prefill_backward", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(dq), _ptr(dk),
           _ptr(dv), _ptr(dg), B, H, N, D, cu_ptr, num_seqs, flags, _ptr(initial_state), _ptr(d_state), _ptr(d_init),
           _ptr(ws), size)
-    _used_on(stream, dq, dk, dv, dg, d_init)
     return (dq, dk, dv, dg) if d_init is None else (dq, dk, dv, dg, d_init)
 
 
@@ -532,18 +565,17 @@ def gated_decode_step(q, k, v, g, state, *, slots=None, out=None, stream=None):
         _is(slots, "slots", torch.int32, dev)
         _need_shape(slots, "slots", (B,))
     flags = _flags_for(dtype)
-    made = out is None
-    if made:
-        out = torch.empty_like(q)
+    here = _aside(dev, stream)
+    if out is None:
+        out = _new(lambda: torch.empty_like(q), stream, here)
     else:
         _need(out, "out", dtype, dev)
         _need_shape(out, "out", shape)
         if any(_overlap(out, t) for t in (q, k, v, g, state) if t is not None):
             raise ValueError("out must not overlap an input or the state")
+    _keep(stream, here, q, k, v, g, state, slots, out)
     _call("la_gated_decode_step", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), B, H, D,
           _ptr(slots), num_slots, flags)
-    if made:
-        _used_on(stream, out)
     return out
 
 
