@@ -232,29 +232,6 @@ __device__ __forceinline__ void split_chunk(const uint4 &raw, float w, bool keep
     for (int y = 0; y < PARTS; ++y) part[y] = make_uint4(out[y][0], out[y][1], out[y][2], out[y][3]);
 }
 
-// Eight lanes that hold eight 16-byte chunks of a row each exchange them, so that chunk k of
-// lane l becomes chunk l % 8 of lane (l - l % 8) + k's row: a warp's 16-byte stores then cover
-// four rows of 128 bytes instead of touching 32 rows (32 passes of the memory pipe) each.
-__device__ __forceinline__ void transpose_chunks(uint4 (&c)[8]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int s = 4; s > 0; s >>= 1) {
-        const bool up = (lane & s) != 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j & s) continue;
-            uint4 a = c[j], b = c[j ^ s];
-            uint4 send = up ? a : b;
-            send.x = __shfl_xor_sync(0xffffffffu, send.x, s);
-            send.y = __shfl_xor_sync(0xffffffffu, send.y, s);
-            send.z = __shfl_xor_sync(0xffffffffu, send.z, s);
-            send.w = __shfl_xor_sync(0xffffffffu, send.w, s);
-            c[j] = up ? send : a;
-            c[j ^ s] = up ? b : send;
-        }
-    }
-}
-
 __device__ __forceinline__ uint4 pack_chunk(const float *x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                       pack_bf16x2(x[6], x[7]));
