@@ -40,7 +40,7 @@ namespace la {
 
 struct GatedBackwardParams {
     CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;  // [T][H*D], box 64 x 128
-    CUtensorMap tmap_s, tmap_ds;                  // [blocks * H * D][D], box 64 x D
+    CUtensorMap tmap_s, tmap_ds;                  // [blocks * H][2 parts][D][D], box 64 x D
     const __nv_bfloat16 *g;
     const float *through;  // [blocks][H][8 D / 64] parts of e^{G_C} <dS, S>, or nullptr
     __nv_bfloat16 *dq, *dk, *dv, *dg;
@@ -62,11 +62,15 @@ struct GatedBackwardCfg {
     static constexpr int OFF_S = 4 * TILE, OFF_DS = OFF_S + PT;
     static constexpr int OFF_P = D == 128 ? OFF_V : OFF_DS + PT;  // D = 64: v is too small for P
     static constexpr int OFF_DP = OFF_S;
-    static constexpr int OFF_STAGE = OFF_S + 2 * PT + (D == 128 ? 0 : PT);  // 2 KB per storing warp
-    static constexpr int OFF_F = OFF_STAGE + 12 * 2048;                     // 9 arrays of 128 floats
+    // The second parts of S and dS.  D = 64: behind the first ones.  D = 128 (STREAM): a slot of
+    // 64 columns, through which those of dS and then of S pass, LOWS in all.
+    static constexpr bool STREAM = D == 128;
+    static constexpr int OFF_LOW = OFF_S + 2 * PT + (D == 128 ? 0 : PT);
+    static constexpr int OFF_STAGE = OFF_LOW + (STREAM ? SBOX : 0);         // 1 KB per storing warp
+    static constexpr int OFF_F = OFF_STAGE + 12 * 1024;                     // 9 arrays of 128 floats
     static constexpr int OFF_MISC = OFF_F + 9 * 512;
     static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
-    static_assert(DB * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
+    static_assert((STREAM ? DB : 2) * SBOX <= PT && (D != 128 || TILE == PT), "places of P and dP");
     static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     static constexpr int TM_S = 0, TM_T = 128, TM_DQ = 256, TM_DK = 384, TM_DV1 = 0, TM_DV2 = 128;
     static constexpr int GROUP_A = 256, GROUP_B = 128, THREADS = 96 + GROUP_A + GROUP_B;
@@ -78,8 +82,10 @@ struct GatedBackwardCfg {
 
 struct GatedBackwardMisc {
     uint64_t full_vo, full_k, full_qs, full_ds;  // v, do; k; q, S; dS landed
+    uint64_t low_full, low_free;          // STREAM: 64 columns of a second part landed, multiplied
+    uint64_t low_done;                    // STREAM: do S^T with S's second part too
     uint64_t gates;                       // gate sums of the block written
-    uint64_t first_full;                  // s, t, do S^T, v dS^T
+    uint64_t first_full;                  // s, t, do S^T (STREAM: of S's first part), v dS^T
     uint64_t s_free;                      // group A has read s and t
     uint64_t p_ready, scaled;             // P and dP written; first terms of dq and dk scaled
     uint64_t dv1_full, dv_full, dq_full, out_full;  // k dS; dv; dq; dk, and with it every product
@@ -131,6 +137,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         mbar_init(&m->full_k, 1);
         mbar_init(&m->full_qs, 1);
         mbar_init(&m->full_ds, 1);
+        mbar_init(&m->low_full, 1);
+        mbar_init(&m->low_free, 1);
+        mbar_init(&m->low_done, 1);
         mbar_init(&m->dv1_full, 1);
         mbar_init(&m->gates, 32);
         mbar_init(&m->first_full, 1);
@@ -170,8 +179,9 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         return warp_wait(bar, parity, abort_flag, tlimit);
     };
     // Loads by warp 0, each as soon as its place is free: dS once k dS is done, v and do once dv
-    // is, k once dq is, q and S once dk is.
-    int n_ds = 0, n_vo = 0, n_k = 0, n_qs = 0;
+    // is, k once dq is, q and S once dk is; columns of the second parts one after the other.
+    int n_ds = 0, n_vo = 0, n_k = 0, n_qs = 0, n_low = 0;
+    const int ds_lows = C::STREAM && p.have_ds ? 2 : 0, lows = ds_lows + (C::STREAM && p.have_s ? 2 : 0);
     auto boxes = [&](int to, const CUtensorMap *map, int col, int row, int box, uint64_t *bar) {
 #pragma unroll 1
         for (int d = 0; d < C::DB; ++d) tma_load_2d(sbase + to + d * box, map, col + 64 * d, row, bar);
@@ -183,11 +193,22 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         row = start + blk * C::C;
         col = (x % p.H) * D;
     };
+    // part y of tile x's state in a tensor of snapshots
+    auto part_row = [](int x, int y) { return (2 * x + y) * D; };
     auto load_ds = [&](int x) {
         ++n_ds;
         if (lane != 0) return;
-        mbar_arrive_expect_tx(&m->full_ds, p.have_ds * C::DB * C::SBOX);
-        if (p.have_ds) boxes(C::OFF_DS, &p.tmap_ds, 0, x * D, C::SBOX, &m->full_ds);
+        mbar_arrive_expect_tx(&m->full_ds, p.have_ds * (C::STREAM ? C::DB : 2) * C::SBOX);
+        if (!p.have_ds) return;
+        boxes(C::OFF_DS, &p.tmap_ds, 0, part_row(x, 0), C::SBOX, &m->full_ds);
+        if (!C::STREAM) boxes(C::OFF_DS + C::SBOX, &p.tmap_ds, 0, part_row(x, 1), C::SBOX, &m->full_ds);
+    };
+    auto load_low = [&](int x, int i) {
+        ++n_low;
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(&m->low_full, C::SBOX);
+        tma_load_2d(sbase + C::OFF_LOW, i < ds_lows ? &p.tmap_ds : &p.tmap_s, 64 * (i & 1), part_row(x, 1),
+                    &m->low_full);
     };
     auto load_vo = [&](int row, int col) {
         ++n_vo;
@@ -205,9 +226,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     auto load_qs = [&](int x, int row, int col) {
         ++n_qs;
         if (lane != 0) return;
-        mbar_arrive_expect_tx(&m->full_qs, C::TILE + p.have_s * C::DB * C::SBOX);
+        mbar_arrive_expect_tx(&m->full_qs, C::TILE + p.have_s * (C::STREAM ? C::DB : 2) * C::SBOX);
         boxes(C::OFF_Q, &p.tmap_q, col, row, C::BOX, &m->full_qs);
-        if (p.have_s) boxes(C::OFF_S, &p.tmap_s, 0, x * D, C::SBOX, &m->full_qs);
+        if (!p.have_s) return;
+        boxes(C::OFF_S, &p.tmap_s, 0, part_row(x, 0), C::SBOX, &m->full_qs);
+        if (!C::STREAM) boxes(C::OFF_S + C::SBOX, &p.tmap_s, 0, part_row(x, 1), C::SBOX, &m->full_qs);
     };
     // The next tile's data into L2 while this one computes: shared memory is full, so that its
     // loads can only start when this tile's last product is done.
@@ -219,8 +242,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             tma_prefetch_l2_2d(&p.tmap_k, col + 64 * d, row);
             tma_prefetch_l2_2d(&p.tmap_do, col + 64 * d, row);
             tma_prefetch_l2_2d(&p.tmap_v, col + 64 * d, row);
-            if (p.have_s) tma_prefetch_l2_2d(&p.tmap_s, 64 * d, x * D);
-            if (p.have_ds) tma_prefetch_l2_2d(&p.tmap_ds, 64 * d, x * D);
+#pragma unroll 1
+            for (int y = 0; y < 2; ++y) {
+                if (p.have_s) tma_prefetch_l2_2d(&p.tmap_s, 64 * d, part_row(x, y));
+                if (p.have_ds) tma_prefetch_l2_2d(&p.tmap_ds, 64 * d, part_row(x, y));
+            }
         }
     };
     uint32_t raw[4];  // gates of the next tile, fetched ahead (warp 0)
@@ -237,6 +263,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         load_k(row, col);
         load_qs(blockIdx.x, row, col);
         load_ds(blockIdx.x);
+        if (lows > 0) load_low(blockIdx.x, 0);
         fetch(blockIdx.x);
     }
     const uint32_t leader = elect_leader();
@@ -246,7 +273,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
     // of the next block needs a product of this one behind p_ready, hence group A's waits (and
     // the last one scaled, hence group B's); the next block's products need dv_read, dq_read and
     // dk_read; its sums (p_ready, scaled) dg_done.
-    uint32_t ph = 0, tail_ph = 0;
+    uint32_t ph = 0, tail_ph = 0, low_ph = 0;
     for (int x = blockIdx.x; ok && x < tiles; x += gridDim.x, ph ^= 1u) {
         const int h = x % p.H;
         int rank, blk, start, len, sid;
@@ -271,11 +298,18 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(&m->tail);
             }
+            int row = 0, col = 0;
             if (next < tiles) {
-                int row, col;
                 place(next, row, col);
                 fetch(next);
                 prefetch(next, row, col);
+            }
+            // low_free of a load needs low_full, its wait and its product; the next phase this load
+            for (int i = 1; ok && i <= lows; ++i, low_ph ^= 1u) {
+                if (i == lows && next >= tiles) break;
+                if ((ok = wwait(&m->low_free, low_ph))) load_low(i < lows ? x : next, i < lows ? i : 0);
+            }
+            if (ok && next < tiles) {
                 if ((ok = wwait(&m->dv1_full, ph))) load_ds(next);
                 if (ok && (ok = wwait(&m->dv_full, ph))) load_vo(row, col);
                 if (ok && (ok = wwait(&m->dq_full, ph))) load_k(row, col);
@@ -305,11 +339,25 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 product(C::TM_T, ok_, kk, vk, kk, C::ID_S, D / 16, false);
                 ok = wwait(&m->full_ds, ph) && (first || wwait(&m->dk_read, ph ^ 1u));
             }
+            // STREAM: d += a B^T, 64 columns `half` of a and of the second part of B
+            auto low = [&](uint32_t d, uint64_t a, int half, bool keep) {
+                if (!(ok = ok && wwait(&m->low_full, low_ph))) return;
+                tc_fence_after();
+                product(d, desc_add(a, half * C::BOX), kk, desc_kmajor_sw128(sbase + C::OFF_LOW), ss, C::ID_KK, 4, keep);
+                warp_commit(leader, &m->low_free);
+                low_ph ^= 1u;
+            };
             if (ok) {
                 tc_fence_after();
-                if (p.have_ds)
+                if (p.have_ds) {
                     product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS), ss, C::ID_KK, D / 16, false);
-                ok = wwait(&m->full_k, ph) && wwait(&m->full_qs, ph);
+                    if (!C::STREAM)
+                        product(C::TM_DK, vk, kk, desc_kmajor_sw128(sbase + C::OFF_DS + C::SBOX), ss, C::ID_KK, D / 16,
+                                true);
+                    else
+                        low(C::TM_DK, vk, 0, true);
+                }
+                ok = ok && wwait(&m->full_k, ph) && wwait(&m->full_qs, ph);
             }
             if (ok) {
                 tc_fence_after();
@@ -318,9 +366,23 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             }
             if (ok) {
                 tc_fence_after();
-                if (p.have_s)
+                if (p.have_s) {
                     product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S), ss, C::ID_KK, D / 16, false);
+                    if (!C::STREAM)
+                        product(C::TM_DQ, ok_, kk, desc_kmajor_sw128(sbase + C::OFF_S + C::SBOX), ss, C::ID_KK, D / 16,
+                                true);
+                }
+                if (ds_lows > 0) low(C::TM_DK, vk, 1, true);
+            }
+            if (ok) {
                 warp_commit(leader, &m->first_full);
+                if (C::STREAM && p.have_s) {
+                    low(C::TM_DQ, ok_, 0, true);
+                    low(C::TM_DQ, ok_, 1, true);
+                    if (ok) warp_commit(leader, &m->low_done);
+                }
+            }
+            if (ok) {
                 ok = wwait(&m->s_free, ph);
             }
             if (ok) {
@@ -386,10 +448,11 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             const bool A = warp < 2 + C::GROUP_A / 32;
             const int half = A ? (warp - 2) >> 2 : 0;
             // 64 columns of this warp's rows out of TMEM and into `out`; with `twice`, dv's first
-            // term times w is added.  32 columns at a time pass through the warp's 2 KB of shared
-            // memory (rows of 64 bytes, chunk c of row r at c ^ (r / 2 % 4)), to be stored eight rows
-            // at a time: from registers a store would touch 32 rows, 32 passes of the memory pipe.
-            const uint32_t stage = sbase + C::OFF_STAGE + (warp - 2) * 2048;
+            // term times w is added.  32 columns at a time pass through the warp's 1 KB of shared
+            // memory, 16 rows at a time (rows of 64 bytes, chunk c of row r at c ^ (r / 2 % 4)), to be
+            // stored eight rows at a time: from registers a store would touch 32 rows, 32 passes of the
+            // memory pipe.
+            const uint32_t stage = sbase + C::OFF_STAGE + (warp - 2) * 1024;
             auto store = [&](uint32_t col, bool twice, float w, __nv_bfloat16 *out, int box) {
 #pragma unroll 1
                 for (int cc = 0; cc < 2; ++cc) {
@@ -404,23 +467,29 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                             a[y] = __float_as_uint(fmaf(w, __uint_as_float(b[y]), __uint_as_float(a[y])));
                     }
                     tmem_ld_wait();
-                    __syncwarp();  // the last pass has been read back
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        st_shared_v4(stage + lane * 64 + ((y ^ ((lane >> 1) & 3)) << 4),
-                                     pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
-                                     pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
-                    __syncwarp();
                     const int r0 = lane >> 2, c = lane & 3;
                     __nv_bfloat16 *dst =
                         out + ((size_t)(row0 + 32 * q + r0) * p.H + h) * D + 64 * box + 32 * cc + 8 * c;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int r = 8 * y + r0;
-                        const uint4 v = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-                        if (32 * q + r < nv) *reinterpret_cast<uint4 *>(dst + (size_t)(8 * y) * p.H * D) = v;
+                    for (int z = 0; z < 2; ++z) {
+                        __syncwarp();  // the last pass has been read back
+                        if (lane >> 4 == z) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                st_shared_v4(stage + (lane & 15) * 64 + ((y ^ ((lane >> 1) & 3)) << 4),
+                                             pack_bf16x2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1])),
+                                             pack_bf16x2(__uint_as_float(a[8 * y + 2]), __uint_as_float(a[8 * y + 3])),
+                                             pack_bf16x2(__uint_as_float(a[8 * y + 4]), __uint_as_float(a[8 * y + 5])),
+                                             pack_bf16x2(__uint_as_float(a[8 * y + 6]), __uint_as_float(a[8 * y + 7])));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = 8 * y + r0;  // of the 16
+                            const uint4 v = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                            if (32 * q + 16 * z + r < nv)
+                                *reinterpret_cast<uint4 *>(dst + (size_t)(16 * z + 8 * y) * p.H * D) = v;
+                        }
                     }
                 }
             };
@@ -548,8 +617,13 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                         }
                     };
                     // e^{G_i}, e^{G_C - G_i}
-                    if (p.have_s) scale(C::TM_DQ, ex2(m->sum - sG[i]), C::OFF_Q, r);
-                    if (p.have_ds) scale(C::TM_DK, ex2(sG[i]), C::OFF_K, e);
+                    const float up = ex2(m->sum - sG[i]), down = ex2(sG[i]);
+                    if (p.have_ds) scale(C::TM_DK, down, C::OFF_K, e);
+                    if (C::STREAM && p.have_s) {
+                        ok = wwait(&m->low_done, ph);
+                        tc_fence_after();
+                    }
+                    if (p.have_s) scale(C::TM_DQ, up, C::OFF_Q, r);
                     sR[i] = r;
                     sE[i] = e;
                     tmem_st_wait();
@@ -558,7 +632,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                     // whose rows were read above
                     fence_proxy_async_smem();
                     mbar_arrive(&m->scaled);
-                    ok = wwait(&m->dq_full, ph);
+                    ok = ok && wwait(&m->dq_full, ph);
                 }
                 if (ok) {
                     tc_fence_after();
@@ -577,6 +651,7 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
             if (n > 0) mbar_wait(bar, (uint32_t)((n - 1) & 1), nullptr, tlimit);
         };
         landed(&m->full_ds, n_ds);
+        landed(&m->low_full, n_low);
         landed(&m->full_vo, n_vo);
         landed(&m->full_k, n_k);
         landed(&m->full_qs, n_qs);

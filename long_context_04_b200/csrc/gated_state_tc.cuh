@@ -48,7 +48,7 @@ struct GatedStateParams {
     float *seg_out;             // [segs][H][D][D]: a segment's own end state, or nullptr
     float *seg_total;           // [segs][H]: its summed log-decay
     float *fin;                 // [S][H][D][D] or nullptr: final states
-    CUtensorMap tmap_snap;      // snapshots, [blocks * H * D][D], box 64 x D
+    CUtensorMap tmap_snap;      // snapshots, [blocks * H][2 parts][D][D], box 64 x D
     CUtensorMap tmap_other;     // reverse: the forward snapshots, the same
     int have_snap;
     float *through;             // reverse: [blocks][H][8 D / 64] parts of e^{G_C} <X, state>, or nullptr
@@ -64,17 +64,17 @@ struct GatedStateCfg {
     static constexpr int DB = D / 64;               // 64-column boxes of the left tile
     static constexpr int BOX = C * 128;             // 128 rows x 128 B
     static constexpr int SBOX = D * 128;            // a slice of a state's snapshot
-    static constexpr int STAGE = (DB + 1) * BOX;    // left tile, then the slice (later its first part)
-    static constexpr int NST = 3;
-    static constexpr int OFF_PARTS = NST * STAGE;   // the slice's second and third parts
-    static constexpr int OFF_SNAP = OFF_PARTS + 2 * BOX;                  // snapshots on their way out, two
-    static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: a forward snapshot
-    static constexpr int OFF_G = OFF_OTHER + (REV ? SBOX : 0);            // gate sums, two blocks
+    static constexpr int TILE = DB * BOX;           // the left tile
+    static constexpr int NST = 3, NSB = REV && D == 128 ? 2 : 3;  // slots for left tiles, for slices
+    static constexpr int OFF_B = NST * TILE;        // slices (later their first part)
+    static constexpr int OFF_PARTS = OFF_B + NSB * BOX;                   // the slice's second and third parts
+    static constexpr int OFF_SNAP = OFF_PARTS + 2 * BOX;                  // a snapshot's parts on their way out
+    static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: a forward snapshot's parts
+    static constexpr int OFF_G = OFF_OTHER + (REV ? 2 * SBOX : 0);           // gate sums, two blocks
     static constexpr int OFF_MISC = OFF_G + 2 * C * 4;
     static constexpr int SMEM_USED = 1024 + OFF_MISC + 512;
-    // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
-    static constexpr int SMEM_BYTES = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static constexpr int SMEM_BYTES = SMEM_USED;
+    static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     static constexpr int TMEM_COLS = 256;           // two accumulators of 128 columns
     static constexpr int ACC = 128;
     static constexpr int GROUP = 256, THREADS = 128 + 2 * GROUP;  // threads of the epilogue, of scaling
@@ -103,10 +103,6 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-// Wait until at most one of this thread's committed bulk stores still reads shared memory.
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
 // A wait of a whole warp for a phase: true once every lane has seen it complete, false after
@@ -235,6 +231,19 @@ __device__ __forceinline__ void split_chunk(const uint4 &raw, float w, bool keep
 __device__ __forceinline__ uint4 pack_chunk(const float *x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                       pack_bf16x2(x[6], x[7]));
+}
+
+// Eight fp32 values as two bf16 parts, the second the rounding of what the first leaves: 16 bits.
+__device__ __forceinline__ void two_parts(const float *x, uint4 (&part)[2]) {
+    uint32_t out[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint64_t v = pair_f32(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]));
+        out[0][e] = pack_f32x2(v);
+        out[1][e] = pack_f32x2(sub_f32x2(v, widen_bf16x2(out[0][e])));
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) part[y] = make_uint4(out[y][0], out[y][1], out[y][2], out[y][3]);
 }
 
 // What the kernels keep of a block's log-decays, in shared memory, times log2(e): for token i
@@ -416,7 +425,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
     auto one = [](int t) { return (uint32_t)(t & 1); };
     auto two = [](int t) { return (uint32_t)((t >> 1) & 1); };
     auto three = [](int t) { return (uint32_t)((t / 3) & 1); };
-    auto stage = [&](int t) { return sbase + (uint32_t)((t % 3) * C::STAGE); };
+    auto tile_at = [&](int t) { return sbase + (uint32_t)((t % 3) * C::TILE); };
+    auto slice_at = [&](int t) { return sbase + C::OFF_B + (uint32_t)((t % C::NSB) * C::BOX); };
 
     if (warp < 4) {
         reg_dec<C::R_MISC>();
@@ -426,15 +436,19 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             int issued = 0;
             for (int t = 0; t < nb; ++t) {
                 if (!(ok = wwait(&m->empty[t % 3], three(t) ^ 1u))) break;
+                const int row = start + block_of(t) * C::C, col = h * D;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&m->full[t % 3], (uint32_t)C::STAGE);
-                    const int row = start + block_of(t) * C::C, col = h * D;
+                    mbar_arrive_expect_tx(&m->full[t % 3], (uint32_t)(C::TILE + C::BOX));
 #pragma unroll
                     for (int d = 0; d < C::DB; ++d)
-                        tma_load_2d(stage(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t % 3]);
-                    tma_load_2d(stage(t) + C::DB * C::BOX, &p.tmap_b, col + 64 * vs, row, &m->full[t % 3]);
+                        tma_load_2d(tile_at(t) + d * C::BOX, &p.tmap_a, col + 64 * d, row, &m->full[t % 3]);
+                    if (C::NSB < 3) tma_prefetch_l2_2d(&p.tmap_b, col + 64 * vs, row);
                 }
                 ++issued;
+                // with two slots for slices, the last but one's products have to be done too (their
+                // next phase needs the tile of t + 1)
+                if (C::NSB < 3 && t >= 2 && !(ok = wwait(&m->empty[(t - 2) % 3], three(t - 2)))) break;
+                if (lane == 0) tma_load_2d(slice_at(t), &p.tmap_b, col + 64 * vs, row, &m->full[t % 3]);
             }
             if (!ok) fail();
             // loads that are still in flight land before the CTA ends
@@ -446,8 +460,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             for (int t = 0; ok && t < nb; ++t) {
                 ok = wwait(&m->full[t % 3], three(t)) && (t < 2 || wwait(&m->acc_free[t & 1], two(t - 2)));
                 // [dims][2 x 64 columns] = A^T [part 0 | part 1 + part 2]
-                const uint32_t b = stage(t) + C::DB * C::BOX, parts = sbase + C::OFF_PARTS;
-                const uint64_t ad = desc_mnmajor_sw128(stage(t), C::BOX);
+                const uint32_t b = slice_at(t), parts = sbase + C::OFF_PARTS;
+                const uint64_t ad = desc_mnmajor_sw128(tile_at(t), C::BOX);
                 const uint64_t bd = desc_mnmajor_sw128(b, parts - b), ld = desc_mnmajor_sw128(parts + C::BOX, C::BOX);
                 const uint32_t acc = tmem + C::ACC * (t & 1);
 #pragma unroll 1
@@ -493,9 +507,13 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             for (int t = 0; t < nb; ++t) {
                 if (!(ok = wwait(&m->other_free, one(t) ^ 1u))) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&m->other_full, (uint32_t)C::SBOX);
-                    tma_load_2d(sbase + C::OFF_OTHER, &p.tmap_other, 64 * vs, number_of(t) * D, &m->other_full);
-                    if (t + 1 < nb) tma_prefetch_l2_2d(&p.tmap_other, 64 * vs, number_of(t + 1) * D);
+                    mbar_arrive_expect_tx(&m->other_full, (uint32_t)(2 * C::SBOX));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        tma_load_2d(sbase + C::OFF_OTHER + y * C::SBOX, &p.tmap_other, 64 * vs,
+                                    (2 * number_of(t) + y) * D, &m->other_full);
+                        if (t + 1 < nb) tma_prefetch_l2_2d(&p.tmap_other, 64 * vs, (2 * number_of(t + 1) + y) * D);
+                    }
                 }
                 __syncwarp();
                 // the epilogue frees the place only once this load has landed; the last one:
@@ -530,20 +548,8 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 X[4 * x] = f.x, X[4 * x + 1] = f.y, X[4 * x + 2] = f.z, X[4 * x + 3] = f.w;
             }
         }
-        // reverse: this row of the block's forward snapshot, read a block ahead, so that the one
-        // place for it is refilled meanwhile
-        uint4 o[4];
-        auto take_other = [&](int t) -> bool {
-            if (!wwait(&m->other_full, one(t))) return false;
-            const uint32_t at = sbase + C::OFF_OTHER + (i_ok ? i : 0) * 128;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = ld_shared_v4(at + (((4 * cg + x) ^ (i & 7)) << 4));
-            fence_proxy_async_smem();  // the rows have been read (reads_done), and TMA may write
-            mbar_arrive(&m->other_free);
-            return true;
-        };
         float total = 0.f;
-        bool ok = !through || nb == 0 || take_other(0);
+        bool ok = true;
         // After a failed wait a warp goes on through the blocks without doing anything but meeting
         // the others at the named barriers, so that none waits there for ever.
         for (int t = 0; t < nb; ++t) {
@@ -557,38 +563,58 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 total += G;
             }
             if (ok && through) {
-                // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns
+                // part of e^{G_C} <X, state at the block's start>: this warp's rows and columns.
+                // other_full of t + 1 needs other_free of t.
+                ok = wwait(&m->other_full, one(t));
+                const uint32_t at = sbase + C::OFF_OTHER + (i_ok ? i : 0) * 128;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint32_t in[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
+                    const uint32_t c = at + (((4 * cg + x) ^ (i & 7)) << 4);
+                    const uint4 hi = ld_shared_v4(c), lo = ld_shared_v4(c + C::SBOX);
+                    const uint32_t in[4] = {hi.x, hi.y, hi.z, hi.w}, rest[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        part[e] = fmaf(__uint_as_float(in[e] << 16), X[8 * x + 2 * e], part[e]);
-                        part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), X[8 * x + 2 * e + 1], part[e]);
+                        const float x0 = X[8 * x + 2 * e], x1 = X[8 * x + 2 * e + 1];
+                        part[e] = fmaf(__uint_as_float(in[e] << 16), x0, part[e]);
+                        part[e] = fmaf(__uint_as_float(in[e] & 0xffff0000u), x1, part[e]);
+                        part[e] = fmaf(__uint_as_float(rest[e] << 16), x0, part[e]);
+                        part[e] = fmaf(__uint_as_float(rest[e] & 0xffff0000u), x1, part[e]);
                     }
                 }
                 float f = i_ok ? (part[0] + part[1]) + (part[2] + part[3]) : 0.f;
+                if (ok) {
+                    fence_proxy_async_smem();  // the rows have been read, and TMA may write
+                    mbar_arrive(&m->other_free);
+                }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
-                if (lane == 0) p.through[(size_t)number_of(t) * (8 * C::NVS) + 8 * vs + 4 * cg + q] = decay * f;
+                if (ok && lane == 0)
+                    p.through[(size_t)number_of(t) * (8 * C::NVS) + 8 * vs + 4 * cg + q] = decay * f;
             }
             if (p.have_snap) {
-                // bf16 rows into one of two buffers, whose store of two blocks ago has read it; then
+                // the parts' rows into their place, which the stores of the block before have read; then
                 // one thread stores the slice
-                if (warp == 4 && lane == 0) bulk_wait_read_but_one();
+                if (warp == 4 && lane == 0) bulk_wait_read_all();
                 __syncwarp();
                 named_barrier(1, C::GROUP);
-                const uint32_t at = sbase + C::OFF_SNAP + (t & 1) * C::SBOX;
+                const uint32_t at = sbase + C::OFF_SNAP;
                 if (i_ok) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        st_shared_u4(at + i * 128 + (((4 * cg + x) ^ (i & 7)) << 4), pack_chunk(&X[8 * x]));
+                    for (int x = 0; x < 4; ++x) {
+                        uint4 part[2];
+                        two_parts(&X[8 * x], part);
+                        const uint32_t c = at + i * 128 + (((4 * cg + x) ^ (i & 7)) << 4);
+                        st_shared_u4(c, part[0]);
+                        st_shared_u4(c + C::SBOX, part[1]);
+                    }
                 }
                 fence_proxy_async_smem();
                 named_barrier(1, C::GROUP);
                 if (ok && warp == 4 && lane == 0) {
-                    tma_store_2d(&p.tmap_snap, at, 64 * vs, number_of(t) * D);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        tma_store_2d(&p.tmap_snap, at + y * C::SBOX, 64 * vs, (2 * number_of(t) + y) * D);
                     bulk_commit_group();
                 }
                 __syncwarp();
@@ -607,7 +633,6 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 for (int z = 0; z < 32; ++z)
                     X[z] = fmaf(decay, X[z], __uint_as_float(a[z]) + __uint_as_float(c[z]));
             }
-            if (ok && through && t + 1 < nb) ok = take_other(t + 1);
         }
         if (warp == 4 && lane == 0) bulk_wait_all();
         float *to = nullptr;
@@ -637,7 +662,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
                 ok = false;
                 break;
             }
-            const uint32_t b = stage(t) + C::DB * C::BOX, parts = sbase + C::OFF_PARTS;
+            const uint32_t b = slice_at(t), parts = sbase + C::OFF_PARTS;
             // chunk c of row r lies in one of the row's eight 16-byte places, whichever the
             // swizzle says; all eight are scaled alike
 #pragma unroll 2
@@ -651,7 +676,7 @@ __global__ void __launch_bounds__(GatedStateCfg<D, REV>::THREADS, 1)
             }
             // rows of another sequence: 0 times what they hold could be a NaN
             for (int c = max(nv, 16 * w8) * 8 + lane; c < (16 * w8 + 16) * 8; c += 32)
-                for (int d = 0; d < C::DB; ++d) st_shared_v4(stage(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
+                for (int d = 0; d < C::DB; ++d) st_shared_v4(tile_at(t) + d * C::BOX + c * 16, 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             mbar_arrive(&m->ready[u]);
             __syncwarp();

@@ -294,8 +294,8 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         nblk = (long long)S * t.blocks_per_seq;
         nseg = (long long)S * t.segs_per_seq;
     }
-    // (the snapshots' rows, nblk * H * D, are coordinates of a tensor map)
-    if (T >= (1ll << 31) || nblk * H * D >= (1ll << 31) || nseg * H * slices >= (1ll << 31) ||
+    // (the snapshots' rows, two parts of nblk * H * D, are coordinates of a tensor map)
+    if (T >= (1ll << 31) || 2 * nblk * H * D >= (1ll << 31) || nseg * H * slices >= (1ll << 31) ||
         (long long)pl.ones * H >= (1ll << 31))
         return LA_ERR_UNSUPPORTED;
     t.blocks = (int)nblk;
@@ -306,7 +306,7 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
         at += (n + 255) & ~(size_t)255;
         return o;
     };
-    const size_t state = (size_t)D * D * 4, shot = tc ? state / 2 : state;
+    const size_t state = (size_t)D * D * 4, shot = state;
     // (joined: the table has the sequences without blocks, which count as a segment, last)
     const bool own = !tc && backward && pl.longest <= 1;  // the call's own states serve
     const size_t shots = own ? 0 : (size_t)(pl.joined ? nseg : nblk) * H * shot;
@@ -490,7 +490,7 @@ la_status gated_states_tc(const void *a, const void *b, const void *g, const flo
                           const void *other, float *through, float *fin, int H, long long T, const GatedPlan &pl,
                           uint8_t *ws, bool behind, cudaStream_t stream) {
     la::GatedStateParams p;
-    const long long rows = (long long)pl.tab.blocks * H * D;
+    const long long rows = 2ll * pl.tab.blocks * H * D;  // two parts
     if (!fill_gated_states<D>(p, a, b, g, H, T, pl) ||
         (snap != nullptr && !make_map(&p.tmap_snap, snap, rows, 1, D, D)) ||
         (through != nullptr && !make_map(&p.tmap_other, other, rows, 1, D, D)))
@@ -581,7 +581,7 @@ la_status gated_backward_tc(const void *q, const void *k, const void *v, const v
             return st;
     la::GatedBackwardParams p;
     std::memset(&p, 0, sizeof p);
-    const long long rows = (long long)pl.tab.blocks * H * D;
+    const long long rows = 2ll * pl.tab.blocks * H * D;  // two parts
     if (!make_map(&p.tmap_q, q, T, H, D, C::C) || !make_map(&p.tmap_k, k, T, H, D, C::C) ||
         !make_map(&p.tmap_v, v, T, H, D, C::C) || !make_map(&p.tmap_do, dout, T, H, D, C::C) ||
         (snap != nullptr && !make_map(&p.tmap_s, snap, rows, 1, D, D)) ||
