@@ -8,10 +8,7 @@
 #include <atomic>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
-#include <numeric>
 #include <type_traits>
-#include <vector>
 
 #include "chunk_state.cuh"
 #include "decode.cuh"
@@ -41,17 +38,18 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// (Threads that come first together each ask, and get the same answer.)
 EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
+    static std::atomic<EncodeTiledFn> known{nullptr};
+    EncodeTiledFn fn = known.load(std::memory_order_acquire);
+    if (fn != nullptr) return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+        fn = reinterpret_cast<EncodeTiledFn>(p);
+        known.store(fn, std::memory_order_release);
+    }
     return fn;
 }
 
@@ -71,7 +69,7 @@ bool make_map(CUtensorMap *map, const void *base, long long T, int H, int D, int
 
 // The sequence table of a call: B equal sequences of N tokens, or the packed
 // boundaries cu_seqlens (host array, validated here), ordered longest first so
-// that the block scheduler starts the longest chains first.
+// that the block scheduler starts the longest chains first (equal ones in their order).
 la_status build_seq_table(int B, int N, const int32_t *cu_seqlens, int num_seqs, SeqTable &seqs,
                           long long &T, int &S) {
     std::memset(&seqs, 0, sizeof seqs);
@@ -86,10 +84,12 @@ la_status build_seq_table(int B, int N, const int32_t *cu_seqlens, int num_seqs,
             if (cu_seqlens[s + 1] < cu_seqlens[s]) return LA_ERR_INVALID_ARG;
         S = num_seqs;
         T = N;
-        std::vector<int> order(S);
-        std::iota(order.begin(), order.end(), 0);
-        std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
-            return cu_seqlens[a + 1] - cu_seqlens[a] > cu_seqlens[b + 1] - cu_seqlens[b];
+        // (no allocation, which could throw across the C boundary)
+        int order[LA_MAX_VARLEN_SEQS];
+        for (int s = 0; s < S; ++s) order[s] = s;
+        std::sort(order, order + S, [&](int a, int b) {
+            const int la = cu_seqlens[a + 1] - cu_seqlens[a], lb = cu_seqlens[b + 1] - cu_seqlens[b];
+            return la != lb ? la > lb : a < b;
         });
         seqs.varlen = 1;
         for (int r = 0; r < S; ++r) {
