@@ -237,8 +237,9 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     t.C = C;
     long long blocks = 0;
     pl.longest = 0;
+    auto blocks_of = [&](int len) { return (int)(((long long)len + C - 1) / C); };
     for (int r = 0; r < (t.seqs.varlen ? S : std::min(S, 1)); ++r) {
-        const int nb = ((t.seqs.varlen ? t.seqs.seq_len[r] : N) + C - 1) / C;
+        const int nb = blocks_of(t.seqs.varlen ? t.seqs.seq_len[r] : N);
         pl.longest = std::max(pl.longest, nb);
         blocks += t.seqs.varlen ? nb : (long long)nb * S;
     }
@@ -247,7 +248,7 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     auto segments = [&](long long seg) {
         if (!t.seqs.varlen) return (long long)S * std::max(1ll, (pl.longest + seg - 1) / seg);
         long long n = 0;
-        for (int r = 0; r < S; ++r) n += std::max(1ll, ((t.seqs.seq_len[r] + C - 1) / C + seg - 1) / seg);
+        for (int r = 0; r < S; ++r) n += std::max(1ll, (blocks_of(t.seqs.seq_len[r]) + seg - 1) / seg);
         return n;
     };
     const long long room = resident / ((long long)H * slices);
@@ -279,7 +280,7 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     long long nblk = 0, nseg = 0;
     if (t.seqs.varlen) {
         for (int r = 0; r < S; ++r) {
-            const int nb = (t.seqs.seq_len[r] + C - 1) / C;
+            const int nb = blocks_of(t.seqs.seq_len[r]);
             t.block0[r] = (int)nblk;
             t.seg0[r] = (int)nseg;
             nblk += nb;

@@ -40,3 +40,17 @@ def test_a_plan_does_not_depend_on_the_order_of_the_sequences(L):
         gen.shuffle(lengths)
         assert _order(L, lengths) == want
     assert _order(L, np.sort(lengths)) == want and _order(L, np.full(1024, 300))[0] == api.LA_OK
+
+
+@pytest.mark.parametrize("flags", [0, 1], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("backward", [0, 1], ids=["prefill", "backward"])
+def test_lengths_next_to_2_31_are_refused(L, flags, backward):
+    """2^31 - 1 tokens have more snapshot rows than a coordinate holds: refused, and not counted
+    as no blocks because the rounded-up length left 32 bits."""
+    n = ctypes.c_ulonglong(7)
+    for N in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 127):
+        assert L.la_gated_workspace(1, 1, N, 64, None, 0, flags, backward, ctypes.byref(n)) == api.LA_ERR_UNSUPPORTED
+        cu = np.asarray([0, N], np.int32)
+        assert L.la_gated_workspace(1, 1, N, 64, cu.ctypes.data, 1, flags, backward,
+                                    ctypes.byref(n)) == api.LA_ERR_UNSUPPORTED
+    assert n.value == 7
