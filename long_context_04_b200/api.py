@@ -13,6 +13,7 @@ the call has returned.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -175,6 +176,25 @@ class _on_device:
         return False
 
 
+def _bounds(cu_seqlens):
+    """The boundaries as a host int32 array; what that does not hold is refused, not wrapped."""
+    if isinstance(cu_seqlens, (list, tuple)) and len(cu_seqlens) > 0:
+        try:  # whole numbers of 32 bits alone: the quick way
+            return np.frombuffer(array.array("i", cu_seqlens), dtype=np.int32)
+        except (TypeError, OverflowError):
+            pass
+    given = np.asarray(cu_seqlens)
+    if given.ndim != 1:
+        raise ValueError("cu_seqlens must be one list of S + 1 boundaries")
+    if given.dtype == np.int32:
+        return np.ascontiguousarray(given)
+    with np.errstate(invalid="ignore"):
+        cu = given.astype(np.int32)
+    if (cu != given).any():
+        raise ValueError("cu_seqlens must hold whole numbers below 2^31")
+    return cu
+
+
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     """Whether the byte ranges of two tensors intersect."""
     a0, b0 = a.data_ptr(), b.data_ptr()
@@ -232,7 +252,7 @@ def prefill(q, k, v, *, beta: int = 128, cu_seqlens=None, rmsnorm: bool = False,
         raise ValueError("q must be [B, N, H, D] or [T, H, D]")
     cu = None
     if cu_seqlens is not None:
-        cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+        cu = _bounds(cu_seqlens)
     here = _aside(dev, stream)
     if out is None:
         out = _new(lambda: torch.empty_like(q), stream, here)
@@ -355,7 +375,7 @@ def chunk_state(k, v, *, cu_seqlens=None, state_out=None, stream=None):
         S = 1 if cu_seqlens is None else len(cu_seqlens) - 1
     else:
         raise ValueError("k must be [B, N, H, D] or [T, H, D]")
-    cu = None if cu_seqlens is None else np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    cu = None if cu_seqlens is None else _bounds(cu_seqlens)
     here = _aside(dev, stream)
     if state_out is None:
         state_out = _new(lambda: torch.empty((S, H, D, D), dtype=torch.float32, device=dev), stream, here)
@@ -446,7 +466,7 @@ def _gated_shape(q, k, v, g, cu_seqlens):
         _need_shape(g, "g", shape[:-1])
     if cu_seqlens is None:
         return (B, H, N, D, S), (None, None, 0)
-    cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    cu = _bounds(cu_seqlens)
     return (B, H, N, D, S), (cu, cu.ctypes.data, len(cu) - 1)
 
 
