@@ -13,5 +13,6 @@ from .api import (LA_BF16, LA_FP32, LA_OUT_RMSNORM, LA_WRITE_STATE, LightningErr
                   version)
 
 __all__ = ["prefill", "decode_step", "state_out", "device_status", "gated_prefill",
-           "gated_prefill_backward", "gated_decode_step", "lib", "status_string", "version", "LightningError", "LightningLibraryError", "LA_BF16", "LA_FP32",
-           "LA_OUT_RMSNORM", "LA_WRITE_STATE"]
+           "gated_prefill_backward", "gated_decode_step", "lib", "status_string", "version",
+           "LightningError", "LightningLibraryError", "LA_BF16", "LA_FP32", "LA_OUT_RMSNORM",
+           "LA_WRITE_STATE"]

@@ -65,10 +65,9 @@ struct GatedPrefillCfg {
     static constexpr int OFF_SNAP = OFF_VP + PARTS * BOX;  // D rows x 64 columns
     static constexpr int OFF_G = OFF_SNAP + D * 128;   // gate sums, two blocks
     static constexpr int OFF_MISC = OFF_G + 1024;
-    static constexpr int SMEM_USED = 1024 + OFF_MISC + 512;
-    // above half of the SM's shared memory: two CTAs of one SM would wait for TMEM
-    static constexpr int SMEM_BYTES = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
+    // (two CTAs of one SM would wait for TMEM, of which each takes all 512 columns)
+    static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     // TMEM: two scores buffers, of which P takes the first 64 columns; q S; P v; k^T v', of the
     // first part and of the other two
     static constexpr int TM_S = 0, TM_QS = 256, TM_PV = 320, TM_KV = 384;

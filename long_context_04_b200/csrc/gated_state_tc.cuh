@@ -72,8 +72,7 @@ struct GatedStateCfg {
     static constexpr int OFF_OTHER = OFF_SNAP + 2 * SBOX;                 // reverse: a forward snapshot's parts
     static constexpr int OFF_G = OFF_OTHER + (REV ? 2 * SBOX : 0);           // gate sums, two blocks
     static constexpr int OFF_MISC = OFF_G + 2 * C * 4;
-    static constexpr int SMEM_USED = 1024 + OFF_MISC + 512;
-    static constexpr int SMEM_BYTES = SMEM_USED;
+    static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 512;
     static_assert(SMEM_BYTES > 114 * 1024 && SMEM_BYTES <= 227 * 1024, "one CTA per SM");
     static constexpr int TMEM_COLS = 256;           // two accumulators of 128 columns
     static constexpr int ACC = 128;
