@@ -10,6 +10,9 @@ With ``stream=`` the kernels run on that stream.  The caller orders it behind th
 makes the arguments, and what reads the results behind it.  Memory needs no care: results and
 workspaces come from that stream's pool, and a tensor may be freed on either stream as soon as
 the call has returned.
+
+The functions record nothing for automatic differentiation: their results have no gradient,
+whatever their arguments require.  ``gated_prefill_backward`` computes gradients.
 """
 from __future__ import annotations
 
