@@ -13,6 +13,9 @@ and independent, each uniform within half a step of at most 2^-8 of the value: r
 2^-8 / sqrt(3), two of them sqrt(2 / 3) * 2^-8.  States and fp32 results: sums of fp32 terms in
 blocks, below 2^-24 * sqrt(terms) of the terms' root sum of squares; 1e-5 as elsewhere.
 """
+import ctypes
+
+import numpy as np
 import pytest
 import torch
 
@@ -149,3 +152,33 @@ def test_every_sequence_by_itself(dtype, D):
         check(inputs(cu, 8, D, dtype, 108, "cuda", kind=kind, grad=True, states=True), cu, dtype)
         x = inputs(cu, 8, D, dtype, 109, "cuda", kind=kind, grad=True)
         check(x, cu, dtype)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS, ids=IDS)
+@pytest.mark.parametrize("H,lengths", [(3, [6000, 0, 1, 130]), (48, [1300, 1, 700])], ids=["segments", "chains"])
+def test_workspace_is_not_read(dtype, D, H, lengths):
+    """A workspace full of NaN, exactly as large as asked for, between guards: the same bits, and
+    nothing written beside it."""
+    cu = bounds(lengths)
+    x = inputs(cu, H, D, dtype, 110, "cuda", grad=True, states=True)
+    want = forward(x, cu) + tuple(backward(x, cu))
+    L, flags, c = api.lib(), api.LA_BF16 if dtype == BF else api.LA_FP32, np.asarray(cu, np.int32)
+    shape = (1, H, cu[-1], D, c.ctypes.data, len(lengths), flags)
+    got = [torch.full_like(t, float("nan")) for t in want]
+    p = {n: t.data_ptr() for n, t in x.items()}
+    for back in (0, 1):
+        n = ctypes.c_ulonglong()
+        assert L.la_gated_workspace(*shape, back, ctypes.byref(n)) == api.LA_OK
+        ws = torch.full((n.value + 2048,), 255, dtype=torch.uint8, device="cuda")
+        at = ws.data_ptr() + 1024
+        if back:
+            o = [t.data_ptr() for t in got[2:]]
+            rc = L.la_gated_prefill_backward(p["q"], p["k"], p["v"], p["g"], p["do"], *o[:4], *shape, p["initial"],
+                                             p["d_state"], o[4], at, n.value, torch.cuda.current_stream().cuda_stream)
+        else:
+            rc = L.la_gated_prefill(p["q"], p["k"], p["v"], p["g"], got[0].data_ptr(), *shape, p["initial"],
+                                    got[1].data_ptr(), at, n.value, torch.cuda.current_stream().cuda_stream)
+        assert rc == api.LA_OK
+        ok()
+        assert bool((ws[:1024] == 255).all()) and bool((ws[1024 + n.value:] == 255).all())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

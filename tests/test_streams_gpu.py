@@ -69,3 +69,58 @@ def test_arguments_freed_at_once():
     torch.cuda.synchronize()
     assert api.device_status() == api.LA_OK
     assert torch.equal(got, want)
+
+
+def test_capture_with_a_forked_stream():
+    """A capture whose call runs on a second stream, forked from the captured one and joined."""
+    x = inputs([0, T], H, D, torch.bfloat16, 63, "cuda", grad=True, states=True)
+
+    def call(s=None):
+        a = api.gated_prefill(*(x[n] for n in "qkvg"), initial_state=x["initial"], return_state=True, stream=s)
+        return a + api.gated_prefill_backward(*(x[n] for n in "qkvg"), x["do"], initial_state=x["initial"],
+                                              d_state=x["d_state"], stream=s)
+
+    call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = call(side)
+        here.wait_stream(side)
+    for seed in (64, 65):
+        for n, t in inputs([0, T], H, D, torch.bfloat16, seed, "cuda", grad=True, states=True).items():
+            x[n].copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert api.device_status() == api.LA_OK
+        for a, b in zip(got, call()):
+            assert torch.equal(a, b)
+
+
+def test_captured_decode_reads_the_slots_of_its_replay():
+    x = inputs([0, 4], H, D, torch.bfloat16, 66, "cuda")
+    gen = torch.Generator().manual_seed(9)
+    start = torch.randn(6, H, D, D, generator=gen).cuda()
+    pool, slots = start.clone(), torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    api.gated_decode_step(*(x[n] for n in "qkvg"), pool, slots=slots)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = api.gated_decode_step(*(x[n] for n in "qkvg"), pool, slots=slots)
+    for at in ([5, 3, 0, 1], [2, -1, 4, 5]):
+        pool.copy_(start)
+        slots.copy_(torch.tensor(at, dtype=torch.int32))
+        o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert api.device_status() == api.LA_OK
+        rows = [b for b, s in enumerate(at) if s >= 0]
+        own = start[[at[b] for b in rows]].contiguous()
+        y = api.gated_decode_step(*(x[n][rows].contiguous() for n in "qkvg"), own)
+        torch.cuda.synchronize()
+        assert torch.equal(o[rows], y) and torch.equal(pool[[at[b] for b in rows]], own)
+        rest = [s for s in range(6) if s not in at]
+        assert torch.equal(pool[rest], start[rest])
+        assert all(bool((o[b] == 7).all()) for b, s in enumerate(at) if s < 0)
