@@ -551,9 +551,10 @@ la_status gated_prefill_tc(const void *q, const void *k, const void *v, const vo
     p.timeout_ns = kWaitLimitNs;
     p.tab = pl.tab;
     // Started early, the two slices of a head land on SMs as these come free, not side by side,
-    // which slows a long pass by 1 %: 8 heads of 131072 tokens (114 blocks a segment) take 426 us
-    // and not 431 without; 4 heads of 32768 (15 blocks) 75 and not 78 with.
-    const bool behind = pl.segmented && pl.tab.seg_blocks <= 64;
+    // which slows a long pass more than it saves.  8 heads, D = 128, with and without: 15 blocks a
+    // segment 75 and 78 us, 29 123 and 125, 43 171 and 173; 57 240 and 225, 86 383 and 365, 114 492
+    // and 486.  (4 heads: 29 blocks 147 and 153, 57 257 and 257; D = 64: within the noise.)
+    const bool behind = pl.segmented && pl.tab.seg_blocks <= 48;
     return launch_behind(behind, kern, dim3((unsigned)(pl.tab.segs * H * C::NVS)), C::THREADS, C::SMEM_BYTES,
                          stream, p);
 }
