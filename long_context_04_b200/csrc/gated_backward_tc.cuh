@@ -232,23 +232,6 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
         boxes(C::OFF_S, &p.tmap_s, 0, part_row(x, 0), C::SBOX, &m->full_qs);
         if (!C::STREAM) boxes(C::OFF_S + C::SBOX, &p.tmap_s, 0, part_row(x, 1), C::SBOX, &m->full_qs);
     };
-    // The next tile's data into L2 while this one computes: shared memory is full, so that its
-    // loads can only start when this tile's last product is done.
-    auto prefetch = [&](int x, int row, int col) {
-        if (lane != 0) return;
-#pragma unroll 1
-        for (int d = 0; d < C::DB; ++d) {
-            tma_prefetch_l2_2d(&p.tmap_q, col + 64 * d, row);
-            tma_prefetch_l2_2d(&p.tmap_k, col + 64 * d, row);
-            tma_prefetch_l2_2d(&p.tmap_do, col + 64 * d, row);
-            tma_prefetch_l2_2d(&p.tmap_v, col + 64 * d, row);
-#pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-                if (p.have_s) tma_prefetch_l2_2d(&p.tmap_s, 64 * d, part_row(x, y));
-                if (p.have_ds) tma_prefetch_l2_2d(&p.tmap_ds, 64 * d, part_row(x, y));
-            }
-        }
-    };
     uint32_t raw[4];  // gates of the next tile, fetched ahead (warp 0)
     auto fetch = [&](int x) {
         int rank, blk, start, len, sid;
@@ -298,18 +281,15 @@ __global__ void __launch_bounds__(GatedBackwardCfg<D>::THREADS, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(&m->tail);
             }
-            int row = 0, col = 0;
-            if (next < tiles) {
-                place(next, row, col);
-                fetch(next);
-                prefetch(next, row, col);
-            }
             // low_free of a load needs low_full, its wait and its product; the next phase this load
             for (int i = 1; ok && i <= lows; ++i, low_ph ^= 1u) {
                 if (i == lows && next >= tiles) break;
                 if ((ok = wwait(&m->low_free, low_ph))) load_low(i < lows ? x : next, i < lows ? i : 0);
             }
             if (ok && next < tiles) {
+                int row, col;
+                place(next, row, col);
+                fetch(next);
                 if ((ok = wwait(&m->dv1_full, ph))) load_ds(next);
                 if (ok && (ok = wwait(&m->dv_full, ph))) load_vo(row, col);
                 if (ok && (ok = wwait(&m->dq_full, ph))) load_k(row, col);
