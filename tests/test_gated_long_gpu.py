@@ -182,3 +182,25 @@ def test_workspace_is_not_read(dtype, D, H, lengths):
         ok()
         assert bool((ws[:1024] == 255).all()) and bool((ws[1024 + n.value:] == 255).all())
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("which", ["initial", "d_state", "neither"])
+def test_many_tiles_of_single_blocks(D, which):
+    """Sequences of one block, several tiles per CTA, with a state at one end or at none."""
+    cu = bounds([100, 128, 31, 77] * 15)
+    x = inputs(cu, 9, D, BF, 113, "cuda", kind="mild", grad=True, states=True)
+    for n in ("initial", "d_state"):
+        if n != which:
+            del x[n]
+    got = backward(x, cu)
+    ok()
+    ref = gradients(x, cu)
+    for y, n in zip(got, ("dq", "dk", "dv")):
+        assert worst(y, ref[n], cu) <= 2 * HALF_STEP[BF], n
+    off = norms(got[3].double() - ref["dg"], cu)
+    # without states the pairs of the block alone, fp32 sums as above
+    own = 2.0 ** -8 + 1e-5
+    assert bool((off <= own * norms(ref["dg"], cu) + 2.0 ** -12 * norms(ref["size"], cu)).all())
+    if which == "initial":
+        assert worst(got[4], ref["d_initial"], None) <= 1e-5
