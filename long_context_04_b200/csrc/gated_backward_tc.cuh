@@ -1,6 +1,6 @@
 // Gradients of gated lightning attention on the tensor cores (bf16), one block of 128 tokens
-// of one head at a time: from the bf16 state S at the block's start and the gradient dS of
-// the state at its end (the state scans' snapshots), every block stands alone.
+// of one head at a time: from the state S at the block's start and the gradient dS of the state
+// at its end (the state scans' snapshots, two bf16 parts each), every block stands alone.
 //
 //   scores   s = q k^T, t = do v^T;  P = s (.) decay,  dP = t (.) decay     (j <= i)
 //   dq = e^{G_i} (do S^T)        + dP k
@@ -9,29 +9,34 @@
 //   dg as in gated.cuh, from W = dP (.) s and the row sums of q . dq and k . dk of the first
 //   terms.
 //
-// A persistent CTA per SM.  Shared memory (D = 128): q, k, v, do 32 KB each, S and dS 32 KB
-// each; P takes the place of v and dP that of S once the products that read those are done.
+// The first terms of dq and dk, from whose rows dg's sums come, use both parts of S and dS; the
+// first term of dv, a vector that no sum follows, the first part of dS alone.  P and dP are one
+// bf16 number each, as operands of the last products; W is formed from the fp32 values.
+//
+// A persistent CTA per SM.  Shared memory (D = 128): q, k, v, do 32 KB each, the first parts of S
+// and dS 32 KB each, a slot of 16 KB through which the second parts pass, 64 columns at a time; P
+// takes the place of v and dP that of S once the products that read those are done.
 // TMEM, 512 columns: s, t, dq, dk; the two terms of dv take the places of s and t.  The decays
 // of the first terms differ by row: those of dq and dk are scaled in TMEM and the second
-// products accumulate on top, the two of dv are added on the way out.  Eight products, in
-// this order:
-//   t, v dS^T, s, do S^T  ->  P, dP; scaling  ->  k dS; P^T do; dP k; dP^T q.
+// products accumulate on top, the two of dv are added on the way out.  The products, in this
+// order (lo: of a second part; D = 64 has both parts in place):
+//   t, v dS^T, lo, s, do S^T, lo  ->  P, dP;  lo, lo  ->  scaling;  k dS; P^T do; dP k; dP^T q.
 // P and dP are each stored once, [i][j]: as the left factor of dP k they are read along j, as
 // the transposed left factor of the other two along i.
 //
 // Warps: 0 TMA loads and gate sums; 1 MMA issue; 2-9 (group A) scores -> P, dP, W, then dv and
 // dk out; 10-13 (group B) scaling of the first terms and their row sums, then dq out; 14 dg.
-// Every barrier completes one phase per block.  The next block's tiles are fetched into L2
-// while this one computes, loaded as their places come free, and multiplied (t, s and the
-// first terms) while its results go out.
+// Every barrier completes one phase per block (the slot's as many as parts pass).  The next
+// block's tiles are loaded as their places come free and multiplied (t, s and the first terms)
+// while this one's results go out.  (Fetching them into L2 ahead cost 6 % of a call: the fetches
+// came between the loads that a block waits for.)
 //
-// HBM: 14 D bytes of tiles and results and 4 D^2 / 128 bytes of snapshots per token and head
-// (2304 at D = 128); tensor: 8 products of 512 cycles per block.  At 8192 tokens, 64 heads,
-// D = 128: 242 us, 5.0 TB/s, tensor cores busy for 27 %; with one CTA per SM (shared memory
-// and TMEM are full) the phases of a block that wait for one another bound it.  A call of that
-// size with its two scans takes 424 us; steps on the way: results through shared memory 570,
-// eight warps for the scores 523, tiles fetched into L2 ahead 510, this block's results out
-// under the next one's products and each tile loaded as its place comes free 431.
+// HBM: 14 D bytes of tiles and results and 8 D^2 / 128 bytes of snapshots per token and head
+// (2816 at D = 128); tensor: 10 products of 512 cycles per block.  At 8192 tokens, 64 heads,
+// D = 128: 291 us, 5.1 TB/s, tensor cores busy for 31 %; with one CTA per SM (shared memory
+// and TMEM are full) the phases of a block that wait for one another bound it: without the second
+// parts it took 242 us, and half of the difference is the wait for one load after the other.  A
+// call of that size with its two scans takes 535 us.
 #pragma once
 
 #include "gated_state_tc.cuh"

@@ -10,7 +10,9 @@
 // their own: their rows are scaled apart), and k^T v' with v' the decayed values split into
 // three bf16 parts (see gated_state_tc.cuh): one product of two parts side by side, [part 0 |
 // part 1], and one that adds part 2 to part 1's columns.
-// P goes back to TMEM over the scores it came from and is read there as the left factor.
+// P goes back to TMEM over the scores it came from and is read there as the left factor.  P and
+// the state's snapshot are one bf16 number each, as operands of products whose results are
+// vectors of D entries: o is off by 2.3e-3 instead of 1.7e-3, and its norm does not cancel.
 //
 // Warpgroups (768 threads; registers are moved to the group that holds the state):
 //   0  warp 0 TMA loads; three issuers: warp 1 the scores, warp 2 q S and P v, warp 3 k^T v'

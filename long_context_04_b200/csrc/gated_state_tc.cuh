@@ -3,11 +3,15 @@
 //   forward   X = state at a block's start,        X <- e^{G_C} X + sum_j k_j (e^{G_C - G_j} v_j)^T
 //   reverse   X = state gradient at its end,       X <- e^{G_C} X + sum_i q_i (e^{G_i} do_i)^T
 //
-// over blocks of C = 128 tokens; the bf16 value of X before each update goes to a snapshot
-// per block, from which the block kernels then run independently of each other.  The snapshot
-// is rounded because it is an operand of bf16 products; X itself stays fp32 from block to
-// block, so that the rounding (2^-9 of an element, as that of any bf16 operand) is not
-// carried on.
+// over blocks of C = 128 tokens; the value of X before each update goes to a snapshot per block,
+// from which the block kernels then run independently of each other.  A snapshot is an operand
+// of bf16 products, so it is left as two bf16 parts, the second the rounding of what the first
+// leaves (16 bits).  One part would do for vectors of D entries, but not for the gate's gradient,
+// one number per token and head whose terms <dS, S>, q . S do and k . dS v may cancel: with it
+// a fifth to two fifths of the heads of up to 1000 tokens with a long memory were off by more
+// than 1.5 times the rounding of the result, some by eight times; with two parts it is the
+// rounding alone.  They cost their traffic: 8192 tokens, 64 heads, D = 128, the two scans together 249 us
+// instead of 206.  X itself stays fp32 from block to block.
 //
 // One CTA per (segment, head, 64-column slice of the state).  Per block the tile of the left
 // factor (128 x D) and the slice of the right one (128 x 64) arrive by TMA; eight warps scale
@@ -19,20 +23,20 @@
 // accumulators to the fp32 state in its registers and stores the snapshots by TMA.
 //
 // The tensor work (3 x 2 D^2 flops per token) is below its HBM time: 4 D bytes read (the left
-// tile is read by D / 64 CTAs, mostly from L2) and 2 D^2 / 128 bytes of snapshot written per
-// token and head; the reverse scan reads as many bytes of forward snapshots again.  What
-// bounds it is the chain of one block after the other.  At 8192 tokens, 64 heads, D = 128 the
-// forward scan takes 92 us (403 MB, 4.4 TB/s; 1.44 us a block) and the reverse one 113 us
-// (537 MB, 4.8 TB/s), the tensor cores busy for 27 and 22 % of it.
+// tile is read by D / 64 CTAs, mostly from L2) and 4 D^2 / 128 bytes of snapshot written per
+// token and head; the reverse scan reads as many bytes of forward snapshots again.  At 8192
+// tokens, 64 heads, D = 128 the forward scan takes 105 us (537 MB, 5.1 TB/s; 1.64 us a block),
+// bound by the chain of one block after the other, and the reverse one 144 us (805 MB, 5.6 TB/s,
+// 85 % of the copy rate), the tensor cores of its 128 SMs busy for 28 and 21 % of it.
 //
 // Warpgroups (640 threads; registers are moved to those that hold the state):
 //   0  warp 0 loads of the tiles; warp 1 MMA issue; warp 2 gate sums; warp 3 loads of the forward
 //      snapshots (reverse scan)
 //   1, 2  epilogue, 32 columns each: the state, its snapshots, in the reverse scan the parts of
-//      e^{G_C} <X, state>.  (With one warpgroup for all 64 columns the two scans together took
-//      7 us more.)
-//   3, 4  scaling.  (With one warpgroup instead of two a backward call took 510 us, not 464.)
-// Three slots for the tiles: with two the next tile came too late (464 us, not 446).
+//      e^{G_C} <X, state>.  (Before snapshots had two parts, one warpgroup for all 64 columns cost
+//      the two scans together 7 us.)
+//   3, 4  scaling.  (At that time a backward call took 464 us, with one warpgroup 510.)
+// Three slots for the tiles: with two the next tile came too late (446 and 464 us).  The reverse scan at D = 128 has room for two slices of 64 columns only.
 #pragma once
 
 #include "gated.cuh"

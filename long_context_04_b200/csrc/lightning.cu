@@ -200,13 +200,14 @@ la_status plan_gated(int B, int H, int N, int D, const int32_t *cu_seqlens, int 
     int S = 0;
     GatedTable &t = pl.tab;
     if (la_status st = build_seq_table(B, N, cu_seqlens, num_seqs, t.seqs, T, S); st != LA_OK) return st;
-    // tensor cores: 128-token blocks, bf16 snapshots (of the backward pass alone: the prefill
-    // kernel keeps its state on chip); CUDA cores: 64-token blocks, fp32 snapshots
-    // The backward pass of a few short sequences runs on the CUDA cores whatever the type, with
-    // scores and states in fp32: over few tokens their bf16 roundings do not average out (up to
-    // 3.8 times the rounding of the result were seen).  It is one or two kernels instead of three:
-    // 64 heads, 16 tokens take 19 us and not 21 at D = 64, 13 us and not 12 (with states 37 and
-    // not 27) at D = 128; from 300 (sequence, head) pairs on it takes longer.
+    // tensor cores: 128-token blocks, snapshots in two bf16 parts (of the backward pass alone: the
+    // prefill kernel keeps its state on chip); CUDA cores: 64-token blocks, fp32 snapshots
+    // The backward pass of a few short sequences runs on the CUDA cores whatever the type.  It is
+    // one or two kernels instead of three: 16 tokens of 64 heads take 10 us of GPU time and not 12
+    // at D = 64 (with states 21 and not 23), 14 and 14 (37 and 31) at D = 128; of 256 (sequence,
+    // head) pairs 13 and not 19 (29 and 41), 27 and 25 (78 and 79).  And scores stay fp32: P of one
+    // token is a single number, whose bf16 rounding shifts a whole row of dk or dv (1.3 times the
+    // result's own rounding in the median, 3 times at most; here 1.0).
     const int most = t.seqs.varlen ? (S > 0 ? t.seqs.seq_len[0] : 0) : N;
     pl.simt = (flags & LA_BF16) == 0 || (backward && most <= kShortTokens && (long long)S * H <= kShortRows);
     const bool tc = !pl.simt;
